@@ -1,11 +1,16 @@
 """Single-precision matrix product C = A·B on MI355X (gfx950), behind a C ABI.
 
 The library (``libsgemm_f32.so``, built from ``csrc/`` by ``build.py``) exports
-the entry points of ``include/sgemm_f32.h``; ``_binding`` mirrors them one to
-one.  ``matmul`` is a convenience for torch tensors: torch provides the device
-memory and the stream, the library does all of the arithmetic.
+the entry points of ``include/*.h``; ``_binding`` mirrors them one to one.
+``matmul`` is a convenience for torch tensors: torch provides the device memory
+and the stream, the library does all of the arithmetic.  ``w4`` (products with
+4-bit weights) and ``experts`` (the products of several matrices in one call, and
+rows sorted by expert) are the same for the other headers.
 """
 from __future__ import annotations
+
+import importlib
+import importlib.util
 
 from ._binding import (ALGO_AUTO, ALGO_BF16X6, ALGO_COUNT, ALGO_LDS_TILED, ALGO_MFMA, ALGO_NAIVE,
                        ALGO_SKINNY, ALGO_SKINNY_N, ALGO_VALU_REGBLOCK, ALGOS, EXPORTED, LIB_PATH,
@@ -14,14 +19,42 @@ from ._binding import (ALGO_AUTO, ALGO_BF16X6, ALGO_COUNT, ALGO_LDS_TILED, ALGO_
                        sgemm_f32_ex_mfma_tile, sgemm_f32_mfma_select, sgemm_f32_mfma_tile,
                        sgemm_f32_mfma_tile_name, sgemm_f32_mfma_tiles, sgemm_f32_select,
                        sgemm_f32_auto_plan, sgemm_f32_ex_ws, sgemm_f32_workspace_size,
-                       sgemm_f32_ex_noalloc, SCRATCH_BYTES)
+                       sgemm_f32_ex_noalloc, SCRATCH_BYTES, W4_SCALE_BF16, W4_SCALE_F16,
+                       W4_SCALE_F32, sgemm_f32_grouped, sgemm_f32_grouped_ta,
+                       sgemm_f32_route_combine, sgemm_f32_route_combine_grad,
+                       sgemm_f32_route_gather, sgemm_f32_route_sort,
+                       sgemm_f32_route_workspace_size, sgemm_f32_w4, sgemm_f32_w4_experts,
+                       sgemm_f32_w4_pack, sgemm_f32_w4_packed_size, sgemm_f32_w4_quantize,
+                       sgemm_f32_w4_unpack)
 
 __all__ = ["matmul", "sgemm_f32", "sgemm_f32_algo", "sgemm_f32_select", "sgemm_f32_algo_name",
            "sgemm_f32_ex", "sgemm_f32_ex_algo", "sgemm_f32_colmajor", "sgemm_f32_mfma_tiles",
            "sgemm_f32_mfma_tile_name", "sgemm_f32_mfma_select", "sgemm_f32_mfma_tile",
            "sgemm_f32_ex_mfma_tile", "sgemm_f32_auto_plan", "sgemm_f32_workspace_size", "sgemm_f32_ex_ws",
            "sgemm_f32_ex_noalloc", "SCRATCH_BYTES", "SgemmError", "ALGOS", "LIB_PATH", "EXPORTED", "lib",
-           "OP_N", "OP_T"]
+           "OP_N", "OP_T", "sgemm_f32_grouped", "sgemm_f32_grouped_ta", "sgemm_f32_route_combine",
+           "sgemm_f32_route_combine_grad", "sgemm_f32_route_gather", "sgemm_f32_route_sort",
+           "sgemm_f32_route_workspace_size", "sgemm_f32_w4", "sgemm_f32_w4_experts",
+           "sgemm_f32_w4_pack", "sgemm_f32_w4_packed_size", "sgemm_f32_w4_quantize",
+           "sgemm_f32_w4_unpack", "W4_SCALE_F32", "W4_SCALE_F16", "W4_SCALE_BF16"]
+
+# The operators for torch tensors, imported when first used: without torch the
+# package is the C binding alone.
+_OPERATORS = {"experts": ("Routing", "sort_by_expert", "gather_rows", "combine_rows",
+                          "combine_rows_grad", "grouped_matmul", "grouped_matmul_ta"),
+              "w4": ("W4Weights", "w4_pack", "w4_quantize", "w4_unpack", "matmul_w4")}
+
+if importlib.util.find_spec("torch") is not None:
+    __all__ += [name for names in _OPERATORS.values() for name in names]
+
+
+def __getattr__(name):
+    for module, names in _OPERATORS.items():
+        if name in names:
+            m = importlib.import_module("." + module, __name__)
+            globals().update({n: getattr(m, n) for n in names})
+            return globals()[name]
+    raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
 
 
 def _layout(rows, cols, s0, s1, name):

@@ -1,4 +1,4 @@
-"""ctypes binding of include/sgemm_f32.h: the same entry points, same arguments.
+"""ctypes binding of include/*.h: the same entry points, same arguments.
 
 This layer only marshals arguments.  Every step of the product runs in the HIP
 kernels of libsgemm_f32.so; there is no fallback of any kind, and a missing
@@ -35,9 +35,18 @@ EXPORTED = ("sgemm_f32", "sgemm_f32_algo", "sgemm_f32_select", "sgemm_f32_algo_n
             "sgemm_f32_ex", "sgemm_f32_ex_algo", "sgemm_f32_colmajor",
             "sgemm_f32_mfma_tiles", "sgemm_f32_mfma_tile_name", "sgemm_f32_mfma_select",
             "sgemm_f32_mfma_tile", "sgemm_f32_ex_mfma_tile", "sgemm_f32_auto_plan",
-            "sgemm_f32_workspace_size", "sgemm_f32_ex_ws", "sgemm_f32_ex_noalloc")
+            "sgemm_f32_workspace_size", "sgemm_f32_ex_ws", "sgemm_f32_ex_noalloc",
+            "sgemm_f32_route_workspace_size", "sgemm_f32_route_sort", "sgemm_f32_route_gather",
+            "sgemm_f32_route_combine", "sgemm_f32_route_combine_grad", "sgemm_f32_grouped",
+            "sgemm_f32_grouped_ta", "sgemm_f32_w4_packed_size", "sgemm_f32_w4_pack",
+            "sgemm_f32_w4_quantize", "sgemm_f32_w4_unpack", "sgemm_f32_w4",
+            "sgemm_f32_w4_experts")
 
 SCRATCH_BYTES = 32 << 20   # SGEMM_F32_SCRATCH_BYTES
+
+W4_SCALE_F32 = 0
+W4_SCALE_F16 = 1
+W4_SCALE_BF16 = 2
 
 _lib = None
 
@@ -101,6 +110,25 @@ def lib() -> ctypes.CDLL:
         ip = ctypes.POINTER(i)
         l.sgemm_f32_auto_plan.argtypes = [i, i, i, i, i, i, ip, ip]
         l.sgemm_f32_auto_plan.restype = i
+        ll, sz = ctypes.c_longlong, ctypes.c_size_t
+        for name, types in {
+                "sgemm_f32_route_sort": [i, i, i, vp, i, vp, vp, vp, vp, sz, vp],
+                "sgemm_f32_route_gather": [i, i, i, vp, vp, i, vp, i, vp],
+                "sgemm_f32_route_combine": [i, i, i, vp, vp, i, vp, i, vp, i, vp],
+                "sgemm_f32_route_combine_grad": [i, i, i, vp, vp, i, vp, i, vp, i, vp, i, vp, vp],
+                "sgemm_f32_grouped": [i, i, i, i, i, vp, f, vp, i, vp, i, ll, f, vp, i, vp],
+                "sgemm_f32_grouped_ta": [i, i, i, i, vp, f, vp, i, vp, i, f, vp, i, ll, vp],
+                "sgemm_f32_w4_pack": [i, i, i, i, vp, vp, i, vp, vp, sz, vp],
+                "sgemm_f32_w4_quantize": [i, i, i, i, vp, i, ll, i, i, vp, sz, vp],
+                "sgemm_f32_w4_unpack": [i, i, i, i, i, i, vp, sz, vp, i, ll, vp],
+                "sgemm_f32_w4": [i, i, i, vp, i, vp, i, i, i, vp, i, vp],
+                "sgemm_f32_w4_experts": [i, i, i, i, vp, vp, i, vp, i, i, i, vp, i, vp]}.items():
+            getattr(l, name).argtypes = types
+            getattr(l, name).restype = i
+        l.sgemm_f32_route_workspace_size.argtypes = [i, i, i]
+        l.sgemm_f32_route_workspace_size.restype = sz
+        l.sgemm_f32_w4_packed_size.argtypes = [i, i, i, i, i, i]
+        l.sgemm_f32_w4_packed_size.restype = sz
         _lib = l
     return _lib
 
@@ -200,3 +228,87 @@ def sgemm_f32_ex_mfma_tile(transa, transb, M, N, K, alpha, A, lda, B, ldb, beta,
     """The general form on the matrix-core rung with configuration `tile`."""
     return lib().sgemm_f32_ex_mfma_tile(transa, transb, M, N, K, alpha, A, lda, B, ldb, beta, C,
                                         ldc, stream, tile)
+
+
+def sgemm_f32_route_workspace_size(tokens, top, experts) -> int:
+    """Bytes of workspace sgemm_f32_route_sort needs (may be 0); no GPU work."""
+    return lib().sgemm_f32_route_workspace_size(tokens, top, experts)
+
+
+def sgemm_f32_route_sort(tokens, top, experts, ids, ldids, offsets, order, position, workspace,
+                         workspace_bytes, stream=0) -> int:
+    """The order of (token, choice) pairs by expert; returns the hipError_t."""
+    return lib().sgemm_f32_route_sort(tokens, top, experts, ids, ldids, offsets, order, position,
+                                      workspace, workspace_bytes, stream)
+
+
+def sgemm_f32_route_gather(tokens, top, width, order, x, ldx, rows, ldrows, stream=0) -> int:
+    """Tokens' rows in the order of their experts; returns the hipError_t."""
+    return lib().sgemm_f32_route_gather(tokens, top, width, order, x, ldx, rows, ldrows, stream)
+
+
+def sgemm_f32_route_combine(tokens, top, width, position, weights, ldw, rows, ldrows, out, ldout,
+                            stream=0) -> int:
+    """Each token's rows, weighted and added; returns the hipError_t."""
+    return lib().sgemm_f32_route_combine(tokens, top, width, position, weights, ldw, rows, ldrows,
+                                         out, ldout, stream)
+
+
+def sgemm_f32_route_combine_grad(tokens, top, width, position, weights, ldw, rows, ldrows, dout,
+                                 lddout, drows, lddrows, dweights, stream=0) -> int:
+    """The gradient of sgemm_f32_route_combine; returns the hipError_t."""
+    return lib().sgemm_f32_route_combine_grad(tokens, top, width, position, weights, ldw, rows,
+                                              ldrows, dout, lddout, drows, lddrows, dweights,
+                                              stream)
+
+
+def sgemm_f32_grouped(transb, rows, N, K, experts, offsets, alpha, A, lda, B, ldb, strideb, beta,
+                      C, ldc, stream=0) -> int:
+    """C = alpha*A*op(B_e) + beta*C by expert of the row; returns the hipError_t."""
+    return lib().sgemm_f32_grouped(transb, rows, N, K, experts, offsets, alpha, A, lda, B, ldb,
+                                   strideb, beta, C, ldc, stream)
+
+
+def sgemm_f32_grouped_ta(rows, M, N, experts, offsets, alpha, A, lda, D, ldd, beta, C, ldc,
+                         stridec, stream=0) -> int:
+    """C_e = alpha*A_e^T*D_e + beta*C_e for every expert; returns the hipError_t."""
+    return lib().sgemm_f32_grouped_ta(rows, M, N, experts, offsets, alpha, A, lda, D, ldd, beta,
+                                      C, ldc, stridec, stream)
+
+
+def sgemm_f32_w4_packed_size(experts, N, K, group, scale_type, zeros) -> int:
+    """Bytes of the packed array of 4-bit weights (0: invalid arguments); no GPU work."""
+    return lib().sgemm_f32_w4_packed_size(experts, N, K, group, scale_type, zeros)
+
+
+def sgemm_f32_w4_pack(experts, N, K, group, codes, scales, scale_type, zeros, packed,
+                      packed_bytes, stream=0) -> int:
+    """4-bit codes and their scales into the packed array; returns the hipError_t."""
+    return lib().sgemm_f32_w4_pack(experts, N, K, group, codes, scales, scale_type, zeros, packed,
+                                   packed_bytes, stream)
+
+
+def sgemm_f32_w4_quantize(experts, N, K, group, B, ldb, strideb, scale_type, zeros, packed,
+                          packed_bytes, stream=0) -> int:
+    """fp32 matrices into the packed array; returns the hipError_t."""
+    return lib().sgemm_f32_w4_quantize(experts, N, K, group, B, ldb, strideb, scale_type, zeros,
+                                       packed, packed_bytes, stream)
+
+
+def sgemm_f32_w4_unpack(experts, N, K, group, scale_type, zeros, packed, packed_bytes, B, ldb,
+                        strideb, stream=0) -> int:
+    """The fp32 matrices a packed array stands for; returns the hipError_t."""
+    return lib().sgemm_f32_w4_unpack(experts, N, K, group, scale_type, zeros, packed,
+                                     packed_bytes, B, ldb, strideb, stream)
+
+
+def sgemm_f32_w4(M, N, K, A, lda, packed, group, scale_type, zeros, C, ldc, stream=0) -> int:
+    """C = A*W for 4-bit weights W; returns the hipError_t."""
+    return lib().sgemm_f32_w4(M, N, K, A, lda, packed, group, scale_type, zeros, C, ldc, stream)
+
+
+def sgemm_f32_w4_experts(rows, N, K, experts, offsets, A, lda, packed, group, scale_type, zeros,
+                         C, ldc, stream=0) -> int:
+    """C = A*W_e by expert of the row, for 4-bit weights; returns the hipError_t."""
+    return lib().sgemm_f32_w4_experts(rows, N, K, experts, offsets, A, lda, packed, group,
+                                      scale_type, zeros, C, ldc, stream)

@@ -1,0 +1,73 @@
+"""What the torch layer of the operators shares: checks of tensors, the stream of a
+call, and the library call itself on the tensors' device."""
+from __future__ import annotations
+
+import torch
+
+from ._binding import SgemmError, lib
+
+INT_MAX = 2**31 - 1
+
+
+def matrix(t, rows, cols, name, dtype=torch.float32, device=None):
+    """The row stride of a rows x cols tensor with unit column stride (rows or cols
+    None: any number); raises where it is not one."""
+    if not isinstance(t, torch.Tensor) or t.dtype != dtype or t.dim() != 2:
+        raise TypeError(f"{name} must be a 2-D {str(dtype).split('.')[-1]} torch tensor")
+    place(t, name, device)
+    r, c = t.shape
+    if (rows is not None and r != rows) or (cols is not None and c != cols):
+        raise ValueError(f"{name} has the shape {r} x {c}; "
+                         f"{'any' if rows is None else rows} x {'any' if cols is None else cols} "
+                         "is needed")
+    s0, s1 = t.stride()
+    if r == 0 or c == 0:
+        return max(c, 1)
+    if c > 1 and s1 != 1:
+        raise ValueError(f"{name} needs a unit column stride")
+    if r > 1 and s0 < c:
+        raise ValueError(f"{name}: row stride {s0} is shorter than a row ({c}); "
+                         "broadcast or overlapping views are not supported")
+    ld = s0 if r > 1 else c
+    if ld > INT_MAX or r > INT_MAX:
+        raise ValueError(f"{name} is too large: {r} rows, row stride {ld}")
+    return ld
+
+
+def place(t, name, device):
+    """Raises unless t lives on the GPU (on `device`, if given)."""
+    if not t.is_cuda:
+        raise ValueError(f"{name} must live on the GPU")
+    if device is not None and t.device != device:
+        raise ValueError(f"{name} lives on {t.device}, the other tensors on {device}")
+
+
+def dense(t, shape, name, dtype, device):
+    """Raises unless t is a contiguous tensor of this shape and type."""
+    if not isinstance(t, torch.Tensor) or t.dtype != dtype:
+        raise TypeError(f"{name} must be a {str(dtype).split('.')[-1]} torch tensor")
+    place(t, name, device)
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} has the shape {tuple(t.shape)}; {tuple(shape)} is needed")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+
+
+def call(entry, device, stream, made, *args):
+    """entry(*args, stream) on the tensors' device, on `stream` (default: torch's
+    current stream there).  Tensors allocated for this call (`made`) are marked as
+    used on a stream that is passed in, so that torch's allocator does not hand
+    their memory out before the work there is done."""
+    f = getattr(lib(), entry)
+    if device.index == torch.cuda.current_device():
+        s = stream if stream is not None else torch.cuda.current_stream(device)
+        status = f(*args, s.cuda_stream)
+    else:
+        with torch.cuda.device(device):
+            s = stream if stream is not None else torch.cuda.current_stream(device)
+            status = f(*args, s.cuda_stream)
+    if status != 0:
+        raise SgemmError(status, entry)
+    if stream is not None and isinstance(stream, torch.cuda.Stream):
+        for t in made:
+            t.record_stream(stream)
