@@ -4,6 +4,9 @@ from __future__ import annotations
 
 import torch
 
+from torch._C import _cuda_getCurrentRawStream as raw_stream
+from torch._C import _cuda_getDevice as current_device
+
 from ._binding import SgemmError, lib
 
 INT_MAX = 2**31 - 1
@@ -53,21 +56,29 @@ def dense(t, shape, name, dtype, device):
         raise ValueError(f"{name} must be contiguous")
 
 
+_entries = {}   # library functions by name, looked up once
+
+
 def call(entry, device, stream, made, *args):
     """entry(*args, stream) on the tensors' device, on `stream` (default: torch's
     current stream there).  Tensors allocated for this call (`made`) are marked as
     used on a stream that is passed in, so that torch's allocator does not hand
     their memory out before the work there is done."""
-    f = getattr(lib(), entry)
-    if device.index == torch.cuda.current_device():
-        s = stream if stream is not None else torch.cuda.current_stream(device)
-        status = f(*args, s.cuda_stream)
+    f = _entries.get(entry)
+    if f is None:
+        f = _entries[entry] = getattr(lib(), entry)
+    index = device.index
+    if stream is not None:
+        with torch.cuda.device(index):
+            status = f(*args, stream.cuda_stream)
+        if isinstance(stream, torch.cuda.Stream):
+            for t in made:
+                t.record_stream(stream)
+    elif index == current_device():
+        # the current stream's handle without a Stream object: 0.1 instead of 1.9 us
+        status = f(*args, raw_stream(index))
     else:
-        with torch.cuda.device(device):
-            s = stream if stream is not None else torch.cuda.current_stream(device)
-            status = f(*args, s.cuda_stream)
+        with torch.cuda.device(index):
+            status = f(*args, raw_stream(index))
     if status != 0:
         raise SgemmError(status, entry)
-    if stream is not None and isinstance(stream, torch.cuda.Stream):
-        for t in made:
-            t.record_stream(stream)

@@ -8,10 +8,11 @@
 // 16-byte load a lane fetches a block and its word j is the lane's operand of the
 // j-th 16x16x32 matrix instruction.  Within a word, codes 0 .. 3 are the low
 // halves of bytes 0 .. 3 and codes 4 .. 7 their high halves: two masks give
-// eight bytes, each the code itself.  Scales and zero points are [part][column]
-// with one part for each min(group, 128) values of k; a group longer than a
-// block has its scale in each of its blocks (2 to 5 bytes for 64 of codes), so a
-// strip is read as one run of memory with nothing on the side.
+// eight bytes, each the code itself.  Scales and zero points are [column][part]
+// with one part for each min(group, 128) values of k, so a lane fetches those of
+// its column with one load each; a group longer than a block has its scale in
+// each of its blocks (2 to 5 bytes for 64 of codes), so a strip is read as one
+// run of memory with nothing on the side.
 #pragma once
 
 #include "internal.h"

@@ -45,14 +45,15 @@ __global__ __launch_bounds__(256) void pack_kernel(W4Layout l, int64_t records,
             const int64_t g = ((int64_t)b * kW4Block + (int64_t)q * (kW4Block / l.parts)) / l.group;
             const bool in = n < l.N && g < groups;
             const int64_t at = in ? (e * groups + g) * l.N + n : 0;
-            unsigned char *s = rec + kW4Codes + lane * l.scale_size;
+            const int place = lane % 16 * l.parts + q;
+            unsigned char *s = rec + kW4Codes + place * l.scale_size;
             if (l.scale_size == 4) {
                 *(unsigned *)s = in ? ((const unsigned *)scales)[at] : 0;
             } else {
                 *(unsigned short *)s = in ? ((const unsigned short *)scales)[at] : 0;
             }
             if (l.zeros)
-                rec[kW4Codes + l.parts * kW4Cols * l.scale_size + lane] =
+                rec[kW4Codes + l.parts * kW4Cols * l.scale_size + place] =
                     in ? zeros[at] & 15 : 0;
         }
     }
@@ -89,7 +90,7 @@ __global__ __launch_bounds__(256) void quantize_kernel(W4Layout l, int64_t items
             const int64_t b = k / kW4Block;
             const int part = l.parts > 1 ? (int)(k % kW4Block) / l.group : 0;
             unsigned char *rec = strip + b * l.record;
-            const int at = part * kW4Cols + n % kW4Cols;
+            const int at = n % kW4Cols * l.parts + part;
             s = w4_store_scale(rec + kW4Codes + at * l.scale_size, wide, l.scale_type);
             if (l.zeros) {
                 z = s > 0.0f ? (int)fminf(rintf(-lo / s), 15.0f) : 8;
@@ -127,7 +128,7 @@ __global__ __launch_bounds__(256) void unpack_kernel(W4Layout l, int64_t items,
         const int kb = k % kW4Block, c = n % kW4Cols;
         const unsigned word =
             *(const unsigned *)(rec + 16 * (c + 16 * (kb % 32 / 8)) + 4 * (kb / 32));
-        const int at = kb / (kW4Block / l.parts) * kW4Cols + c;
+        const int at = c * l.parts + kb / (kW4Block / l.parts);
         const float s = w4_scale(rec + kW4Codes + at * l.scale_size, l.scale_type);
         const int z = l.zeros ? rec[kW4Codes + l.parts * kW4Cols * l.scale_size + at] : 8;
         const int q = (word >> w4_shift(kb % 8)) & 15;

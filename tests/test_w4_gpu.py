@@ -111,6 +111,57 @@ def test_product_of_ordinary_sizes(rows, N, K):
         close(run(x, w), x.astype(np.float64) @ W[0], K, np.abs(x.astype(np.float64)) @ mag[0], "w4")
 
 
+@pytest.mark.parametrize("rows,N,K,group", [(1000, 1500, 300, 32), (801, 2047, 129, 64),
+                                            (513, 2900, 1030, 128), (6200, 256, 4, 32)])
+def test_product_of_many_rows(rows, N, K, group):
+    """Sizes at which the kernel for many rows runs (192 work-groups of 32 x 256)."""
+    torch = torch_cuda()
+    rng = np.random.default_rng(rows)
+    for zeros, scale_type, exact in [(True, "float32", True), (False, "bfloat16", False),
+                                     (True, "float16", False)]:
+        log(f"[gpu] w4 {rows} x {N} x {K} group {group} {scale_type} zeros {zeros}")
+        codes, s, z, W, mag = make(rng, 1, K, N, group, zeros, exact, scale_type)
+        w = sg.w4_pack(codes[0], s[0], None if z is None else z[0], K=K, group=group)
+        x = rng.integers(-4, 5, (rows, K)).astype(np.float32) if exact else \
+            rng.standard_normal((rows, K)).astype(np.float32)
+        got = run(x, w, pad=1, offset=3)
+        if exact:
+            assert np.array_equal(got.double().cpu().numpy(), x.astype(np.float64) @ W[0])
+        else:
+            close(got, x.astype(np.float64) @ W[0], K, np.abs(x.astype(np.float64)) @ mag[0], "w4")
+
+
+@pytest.mark.parametrize("which", ["one has all", "ragged", "rows of no expert"])
+def test_product_of_many_rows_by_expert(which):
+    torch = torch_cuda()
+    rows, N, K, experts = 900, 1300, 200, 16
+    rng = np.random.default_rng(5)
+    offsets = [int(o) for o in OFFSETS[which](rows, experts)]
+    codes, s, z, W, mag = make(rng, experts, K, N, 64, True, True, "float16")
+    w = sg.w4_pack(codes, s, z, K=K, group=64)
+    x = rng.integers(-4, 5, (rows, K)).astype(np.float32)
+    got = run(x, w, offsets=torch.tensor(offsets, dtype=torch.int32, device="cuda"), pad=3)
+    want = np.full((rows, N), SENT)
+    for e, (lo, hi) in enumerate(zip(offsets, offsets[1:])):
+        want[lo:hi] = x[lo:hi].astype(np.float64) @ W[e]
+    assert np.array_equal(got.double().cpu().numpy(), want)
+
+
+@pytest.mark.parametrize("K", [1, 2, 3, 4, 5, 7, 8])
+def test_product_of_very_few_k(K):
+    torch = torch_cuda()
+    rng = np.random.default_rng(K)
+    for rows, N in [(1, 5), (3, 40), (7, 300), (20, 17), (70, 33)]:
+        for zeros in (False, True):
+            codes, s, z, W, _ = make(rng, 2, K, N, 32, zeros, True, "float32")
+            w = sg.w4_pack(codes, s, z, K=K, group=32)
+            x = rng.integers(-4, 5, (rows, K)).astype(np.float32)
+            lo = rows // 3
+            got = run(x, w, offsets=torch.tensor([0, lo, rows], dtype=torch.int32, device="cuda"), pad=2)
+            want = np.concatenate([x[:lo].astype(np.float64) @ W[0], x[lo:].astype(np.float64) @ W[1]])
+            assert np.array_equal(got.double().cpu().numpy(), want)
+
+
 OFFSETS = {"each one row": lambda R, E: [min(e, R) for e in range(E + 1)],
            "one has all": lambda R, E: [0] * (E // 2 + 1) + [R] * (E - E // 2),
            "ragged": lambda R, E: [0] + sorted(np.random.default_rng(R).integers(0, R + 1, E - 1)) + [R],
