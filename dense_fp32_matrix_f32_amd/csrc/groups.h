@@ -56,6 +56,24 @@ __device__ __forceinline__ bool find_block(const int *__restrict__ offsets, int 
     return false;
 }
 
+// How many blocks there are, for every lane of a wave.
+__device__ __forceinline__ int count_blocks(const int *__restrict__ offsets, int experts, int rows,
+                                            int block) {
+    const int lane = threadIdx.x & 63;
+    int count = 0;
+    for (int base = 0; base < experts; base += 64) {
+        const int e = base + lane;
+        int mine = 0;
+        if (e < experts) {
+            const int lo = clamp_row(offsets[e], rows);
+            const int hi = max(lo, clamp_row(offsets[e + 1], rows));
+            mine = (int)(((int64_t)hi - lo + block - 1) / block);
+        }
+        count += __builtin_amdgcn_readlane(wave_scan(mine), 63);
+    }
+    return count;
+}
+
 // The most blocks find_block() can find: each expert with rows ends at most one
 // block short of full.
 inline int64_t most_blocks(int rows, int experts, int block) {

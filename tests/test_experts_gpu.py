@@ -258,6 +258,51 @@ def test_grouped(rows, N, K, experts, groups):
         assert int((buf != SENT).sum()) == 0, "wrote outside C"
 
 
+@pytest.mark.parametrize("rows,N,K,experts", [(9001, 200, 330, 2), (620, 130, 1030, 4),
+                                              (1500, 300, 333, 16), (90, 530, 2050, 2)])
+def test_grouped_on_larger_blocks(rows, N, K, experts):
+    """Rows an expert at which the larger blocks are taken, k long enough for their
+    steady loops."""
+    torch = torch_cuda()
+    rng = np.random.default_rng(rows)
+    offsets = GROUPS["ragged"](rows, experts)
+    dev_off = torch.from_numpy(offsets.astype(np.int32)).cuda()
+    A, B, D = int_matrix(rng, rows, K), int_matrix(rng, experts, K, N), int_matrix(rng, rows, N)
+    dA, dB, dD = (torch.from_numpy(t).cuda() for t in (A, B, D))
+    for trans in (False, True):
+        mat = dB.transpose(1, 2).contiguous().transpose(1, 2) if trans else dB
+        got = sg.grouped_matmul(dA, mat, dev_off).double().cpu().numpy()
+        want, _ = plain_grouped(A.astype(np.float64), B.astype(np.float64), offsets,
+                                np.zeros((rows, N)), 1.0, 0.0)
+        assert np.array_equal(got, want)
+    got = sg.grouped_matmul_ta(dA, dD, dev_off).double().cpu().numpy()
+    for e, (lo, hi) in enumerate(zip(offsets, offsets[1:])):
+        assert np.array_equal(got[e], A[lo:hi].T.astype(np.float64) @ D[lo:hi])
+
+
+def test_rows_so_long_that_offsets_pass_31_bits():
+    torch = torch_cuda()
+    rng = np.random.default_rng(2)
+    ld, rows, K, N, experts = 36_000_003, 6, 40, 70, 2
+    offsets = np.array([0, 2, 6])
+    dev_off = torch.from_numpy(offsets.astype(np.int32)).cuda()
+    A, B, D = int_matrix(rng, rows, K), int_matrix(rng, experts, K, N), int_matrix(rng, rows, N)
+    wide = torch.empty((rows, ld), device="cuda")
+    dA = wide[:, :K]
+    dA.copy_(torch.from_numpy(A))
+    dB = torch.from_numpy(B).cuda()
+    want, _ = plain_grouped(A.astype(np.float64), B.astype(np.float64), offsets,
+                            np.zeros((rows, N)), 1.0, 0.0)
+    for mat in (dB, dB.transpose(1, 2).contiguous().transpose(1, 2)):
+        out = torch.empty((rows, ld), device="cuda")[:, 5:5 + N]
+        sg.grouped_matmul(dA, mat, dev_off, out=out)
+        assert np.array_equal(out.double().cpu().numpy(), want)
+        del out
+    got = sg.grouped_matmul_ta(dA, torch.from_numpy(D).cuda(), dev_off).double().cpu().numpy()
+    for e, (lo, hi) in enumerate(zip(offsets, offsets[1:])):
+        assert np.array_equal(got[e], A[lo:hi].T.astype(np.float64) @ D[lo:hi])
+
+
 @pytest.mark.parametrize("groups", list(GROUPS))
 @pytest.mark.parametrize("rows,N,M,experts", SHAPES)
 def test_grouped_ta(rows, N, M, experts, groups):
