@@ -242,9 +242,9 @@ def sgemm_f32_route_sort(tokens, top, experts, ids, ldids, offsets, order, posit
                                       workspace, workspace_bytes, stream)
 
 
-def sgemm_f32_route_gather(tokens, top, width, order, x, ldx, rows, ldrows, stream=0) -> int:
+def sgemm_f32_route_gather(tokens, top, width, position, x, ldx, rows, ldrows, stream=0) -> int:
     """Tokens' rows in the order of their experts; returns the hipError_t."""
-    return lib().sgemm_f32_route_gather(tokens, top, width, order, x, ldx, rows, ldrows, stream)
+    return lib().sgemm_f32_route_gather(tokens, top, width, position, x, ldx, rows, ldrows, stream)
 
 
 def sgemm_f32_route_combine(tokens, top, width, position, weights, ldw, rows, ldrows, out, ldout,

@@ -14,8 +14,8 @@ struct Pairs {
 size_t route_workspace(Pairs p, int experts);
 hipError_t launch_route_sort(Pairs p, int experts, const int *ids, int64_t ldids, int *offsets,
                              int *order, int *position, void *workspace, hipStream_t s);
-hipError_t launch_route_gather(Pairs p, int width, const int *order, const float *x, int64_t ldx,
-                               float *rows, int64_t ldrows, hipStream_t s);
+hipError_t launch_route_gather(Pairs p, int width, const int *position, const float *x,
+                               int64_t ldx, float *rows, int64_t ldrows, hipStream_t s);
 hipError_t launch_route_combine(Pairs p, int width, const int *position, const float *weights,
                                 int64_t ldw, const float *rows, int64_t ldrows, float *out,
                                 int64_t ldout, hipStream_t s);

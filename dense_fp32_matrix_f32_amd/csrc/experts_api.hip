@@ -68,19 +68,20 @@ extern "C" hipError_t sgemm_f32_route_sort(int tokens, int top, int experts, con
                                     workspace, stream);
 }
 
-extern "C" hipError_t sgemm_f32_route_gather(int tokens, int top, int width, const int *order,
-                                             const float *x, int ldx, float *rows, int ldrows,
+extern "C" hipError_t sgemm_f32_route_gather(int tokens, int top, int width,
+                                             const int *position, const float *x, int ldx, float *rows, int ldrows,
                                              hipStream_t stream) {
     if (!valid_pairs(tokens, top) || width < 0 || ldx < at_least_one(width) ||
         ldrows < at_least_one(width))
         return hipErrorInvalidValue;
     const int n = tokens * top;
     if (n == 0 || width == 0) return hipSuccess;
-    if (order == nullptr || x == nullptr || rows == nullptr) return hipErrorInvalidValue;
+    if (position == nullptr || x == nullptr || rows == nullptr) return hipErrorInvalidValue;
     if (any_overlap({matrix(rows, n, width, ldrows)},
-                    {list(order, n), matrix(x, tokens, width, ldx)}))
+                    {list(position, n), matrix(x, tokens, width, ldx)}))
         return hipErrorInvalidValue;
-    return sgemm::launch_route_gather({tokens, top}, width, order, x, ldx, rows, ldrows, stream);
+    return sgemm::launch_route_gather({tokens, top}, width, position, x, ldx, rows, ldrows,
+                                      stream);
 }
 
 extern "C" hipError_t sgemm_f32_route_combine(int tokens, int top, int width, const int *position,

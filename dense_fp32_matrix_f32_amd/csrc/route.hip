@@ -1,143 +1,421 @@
 // route.hip -- the order of rows by expert, and rows moved along it.
+//
+// All of it is bound by memory traffic (or, for a few tokens, by the launch).  The
+// pairs (token, choice) are numbered f = token * top + choice.
+#include <type_traits>
+
 #include "experts.h"
+#include "groups.h"
 
 namespace sgemm {
 
 namespace {
 
-constexpr int kSortThreads = 1024;
+typedef float f32x4 __attribute__((ext_vector_type(4)));
 
-// One work-group for each expert: it counts the pairs of the experts below its
-// own, then walks all pairs in order and gives its own the places from there on.
-// A wave ranks its 64 pairs by a ballot, the work-group's waves by a running sum
-// in LDS.  The group `experts` handles what is dropped, which has no places.
-__global__ __launch_bounds__(kSortThreads) void sort_kernel(Pairs p, int experts,
-                                                            const int *__restrict__ ids,
-                                                            int64_t ldids, int *offsets,
-                                                            int *order, int *position) {
-    constexpr int WAVES = kSortThreads / 64;
-    __shared__ int sums[WAVES];
+// ---------------------------------------------------------------------------
+// The order: a counting sort by expert, stable in f.  Dropped pairs count as one
+// more expert after the others, whose places are written as -1.
+//
+// The pairs are cut into chunks, one for each work-group, and a chunk into equal
+// runs, one for each wave.  A work-group counts its chunk's pairs by expert and
+// wave in LDS; adding the counts of the chunks before it and of all smaller experts
+// gives the place of each wave's first pair of each expert, and a wave then walks
+// its run 64 pairs at a time, a pair's rank among equal ones found by comparing
+// the bits of its expert with ballots.  With more than one chunk a first kernel
+// leaves every chunk's counts in the workspace.  No place depends on which
+// work-group or wave runs first.
+constexpr int kSortThreads = 1024, kSortWaves = kSortThreads / 64;
+constexpr int kSortChunks = 128;         // at most
+constexpr int kSortBuckets = 896;        // experts + 1 at most (56 KB of LDS)
+
+struct SortArgs {
+    Pairs p;
+    int experts;
+    const int *ids;
+    int64_t ldids;
+    int run;     // pairs of a wave (a multiple of 64)
+    int chunks;
+    int *counts;  // chunks x (experts + 1), or NULL with one chunk
+};
+
+__device__ __forceinline__ int bucket_of(const SortArgs &a, int f) {
+    const int e = a.ids[(int64_t)(f / a.p.top) * a.ldids + f % a.p.top];
+    return e < 0 || e >= a.experts ? a.experts : e;
+}
+
+// counts of this wave's run into its row of `mine` (cleared before)
+__device__ __forceinline__ void count_run(const SortArgs &a, int begin, int *mine) {
+    const int n = a.p.count(), lane = threadIdx.x & 63;
+    for (int f = begin + lane; f < min(n, begin + a.run); f += 64)
+        atomicAdd(&mine[bucket_of(a, f)], 1);  // sums of ones: any order gives the same
+}
+
+__device__ __forceinline__ int run_begin(const SortArgs &a) {
+    // clamped: a chunk that starts past the last pair is empty
+    const int64_t b = ((int64_t)blockIdx.x * kSortWaves + (threadIdx.x >> 6)) * a.run;
+    return (int)min(b, (int64_t)a.p.count());
+}
+
+__global__ __launch_bounds__(kSortThreads) void sort_count_kernel(SortArgs a) {
+    __shared__ int hist[kSortBuckets];
+    const int buckets = a.experts + 1;
+    for (int e = threadIdx.x; e < buckets; e += kSortThreads) hist[e] = 0;
+    __syncthreads();
+    count_run(a, run_begin(a), hist);
+    __syncthreads();
+    for (int e = threadIdx.x; e < buckets; e += kSortThreads)
+        a.counts[(int64_t)blockIdx.x * buckets + e] = hist[e];
+}
+
+__global__ __launch_bounds__(kSortThreads) void sort_place_kernel(SortArgs a, int *offsets,
+                                                                  int *order, int *position) {
+    extern __shared__ int next[];  // [wave][bucket]: the place of the next pair
+    __shared__ int sums[kSortWaves];
+    const int buckets = a.experts + 1, n = a.p.count();
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    for (int i = tid; i < buckets * kSortWaves; i += kSortThreads) next[i] = 0;
+    __syncthreads();
+    const int begin = run_begin(a);
+    int *mine = next + wave * buckets;
+    count_run(a, begin, mine);
+    __syncthreads();
+
+    // one work-item for each bucket (kSortBuckets <= kSortThreads)
+    int before = 0, all = 0;
+    if (tid < buckets) {
+        if (a.counts != nullptr) {
+            const int *c = a.counts + tid;
+#pragma unroll 8
+            for (int b = 0; b < a.chunks; ++b) {
+                const int v = c[(int64_t)b * buckets];
+                if (b < (int)blockIdx.x) before += v;
+                all += v;
+            }
+        } else {
+            for (int w = 0; w < kSortWaves; ++w) all += next[w * buckets + tid];
+        }
+    }
+    int upto = wave_scan(all);
+    if (lane == 63) sums[wave] = upto;
+    __syncthreads();
+    for (int w = 0; w < wave; ++w) upto += sums[w];
+    if (tid < buckets) {
+        const int first = upto - all;
+        if (blockIdx.x == 0) offsets[tid] = first;
+        int at = first + before;
+        for (int w = 0; w < kSortWaves; ++w) {
+            const int c = next[w * buckets + tid];
+            next[w * buckets + tid] = at;
+            at += c;
+        }
+    }
+    __syncthreads();
+
+    for (int base = begin; base < min(n, begin + a.run); base += 64) {
+        const int f = base + lane;
+        const bool have = f < min(n, begin + a.run);
+        const int e = have ? bucket_of(a, f) : buckets;
+        // the lanes with the same bucket
+        unsigned long long same = __ballot(have);
+        for (int bit = 1; bit < buckets; bit *= 2) {
+            const unsigned long long set = __ballot(e & bit);
+            same &= e & bit ? set : ~set;
+        }
+        if (have) {
+            const unsigned long long below = same & ((1ull << lane) - 1);
+            const int at = mine[e] + __popcll(below);
+            position[f] = e < a.experts ? at : -1;
+            order[at] = e < a.experts ? f : -1;
+        }
+        // the last lane of each bucket moves its place on, after all have read it
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        __builtin_amdgcn_wave_barrier();
+        if (have && (same >> lane) == 1) mine[e] += __popcll(same);
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        __builtin_amdgcn_wave_barrier();
+    }
+}
+
+// More experts than fit LDS: one work-group for each bucket.  It counts the pairs of
+// the buckets below its own, then walks all pairs in order and gives its own the
+// places from there on, ranked by a ballot in a wave and a running sum over waves.
+__global__ __launch_bounds__(kSortThreads) void sort_each_kernel(SortArgs a, int *offsets,
+                                                                 int *order, int *position) {
+    __shared__ int sums[kSortWaves];
     const int me = blockIdx.x, tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-    const int n = p.count();
-    auto id_of = [&](int f) {
-        const int e = ids[(int64_t)(f / p.top) * ldids + f % p.top];
-        return e < 0 || e >= experts ? experts : e;
-    };
+    const int n = a.p.count();
     int below = 0;
-    for (int f = tid; f < n; f += kSortThreads) below += id_of(f) < me;
+    for (int64_t f = tid; f < n; f += kSortThreads) below += bucket_of(a, (int)f) < me;
     for (int d = 32; d; d /= 2) below += __shfl_xor(below, d);
     if (lane == 0) sums[wave] = below;
     __syncthreads();
-    int next = 0;
-    for (int w = 0; w < WAVES; ++w) next += sums[w];
-    if (tid == 0) offsets[me] = next;
+    int place = 0;
+    for (int w = 0; w < kSortWaves; ++w) place += sums[w];
+    if (tid == 0) offsets[me] = place;
     __syncthreads();
-    for (int base = 0; base < n; base += kSortThreads) {
-        const int f = base + tid;
-        const bool mine = f < n && id_of(f) == me;
+    for (int64_t base = 0; base < n; base += kSortThreads) {
+        const int64_t f = base + tid;
+        const bool mine = f < n && bucket_of(a, (int)f) == me;
         const unsigned long long who = __ballot(mine);
         if (lane == 0) sums[wave] = __popcll(who);
         __syncthreads();
-        int at = next;
-        for (int w = 0; w < WAVES; ++w) {
+        int at = place;
+        for (int w = 0; w < kSortWaves; ++w) {
             if (w < wave) at += sums[w];
-            next += sums[w];
+            place += sums[w];
         }
         if (mine) {
             at += __popcll(who & ((1ull << lane) - 1));
-            position[f] = me < experts ? at : -1;
-            order[at] = me < experts ? f : -1;
+            position[f] = me < a.experts ? at : -1;
+            order[at] = me < a.experts ? (int)f : -1;
         }
         __syncthreads();
     }
 }
 
-// One work-group for each place (row) in turn.
-__global__ __launch_bounds__(256) void gather_kernel(Pairs p, int width,
-                                                     const int *__restrict__ order,
+// Pairs of a wave and chunks.  Up to 4096 pairs are one chunk.
+void sort_cut(int64_t n, int *run, int *chunks) {
+    const int64_t least = 256ll * kSortWaves;
+    const int64_t even = (n + kSortChunks - 1) / kSortChunks;
+    const int64_t chunk = n <= least ? n : even < 1024 ? 1024 : even;
+    *run = (int)((chunk + kSortThreads - 1) / kSortThreads * 64);
+    const int64_t per = (int64_t)*run * kSortWaves;
+    *chunks = n > 0 ? (int)((n + per - 1) / per) : 1;
+}
+
+// ---------------------------------------------------------------------------
+// Rows there and back.  The lanes of a row take four columns each (16-byte accesses,
+// which gfx950 takes at any multiple of four bytes).
+
+// Work-items for a row: enough for its vectors, a power of two from 16 to `most`.
+int lanes_for(int width, int most) {
+    int lanes = 16;
+    while (lanes < most && lanes * 4 < width) lanes *= 2;
+    return lanes;
+}
+
+__device__ __forceinline__ f32x4 load4(const float *p) {
+    f32x4 v;
+    __builtin_memcpy(&v, p, 16);
+    return v;
+}
+
+__device__ __forceinline__ void store4(float *p, f32x4 v) { __builtin_memcpy(p, &v, 16); }
+
+// Calls body(c, vector) for this lane's columns of [begin, end): with 16-byte vectors
+// at c, then for the last end % 4 columns one by one on the first lanes.
+template <class Body>
+__device__ __forceinline__ void for_columns(int64_t begin, int64_t end, int lane, int lanes,
+                                            const Body &body) {
+    const int64_t whole = begin + (end - begin) / 4 * 4;
+    for (int64_t c = begin + 4 * lane; c < whole; c += 4 * lanes) body(c, std::true_type{});
+    if (lane < end - whole) body(whole + lane, std::false_type{});
+}
+
+template <bool VECTOR>
+using Cols = typename std::conditional<VECTOR, f32x4, float>::type;
+
+__device__ __forceinline__ f32x4 load(const float *p, std::true_type) { return load4(p); }
+__device__ __forceinline__ float load(const float *p, std::false_type) { return *p; }
+__device__ __forceinline__ void store(float *p, f32x4 v) { store4(p, v); }
+__device__ __forceinline__ void store(float *p, float v) { *p = v; }
+__device__ __forceinline__ f32x4 mul_add(float w, f32x4 v, f32x4 sum) {
+    for (int e = 0; e < 4; ++e) sum[e] = fmaf(w, v[e], sum[e]);
+    return sum;
+}
+__device__ __forceinline__ float mul_add(float w, float v, float sum) { return fmaf(w, v, sum); }
+__device__ __forceinline__ float dot_add(f32x4 a, f32x4 b, float sum) {
+    for (int e = 0; e < 4; ++e) sum = fmaf(a[e], b[e], sum);
+    return sum;
+}
+__device__ __forceinline__ float dot_add(float a, float b, float sum) { return fmaf(a, b, sum); }
+
+constexpr int J = 4;  // choices whose loads are in flight together
+
+// Places and weights of choices j0 .. j0+3 of a token; -1 past the last and where
+// there is none.
+struct Choices {
+    int place[J];
+    float w[J];
+
+    __device__ __forceinline__ Choices(Pairs p, int64_t t, int j0, const int *position,
+                                       const float *weights, int64_t ldw) {
+#pragma unroll
+        for (int j = 0; j < J; ++j) {
+            const int at = j0 + j < p.top ? position[t * p.top + j0 + j] : -1;
+            place[j] = at >= 0 && at < p.count() ? at : -1;
+            w[j] = place[j] >= 0 && weights != nullptr ? weights[t * ldw + j0 + j] : 1.0f;
+        }
+    }
+    // A row to load from without a branch: a choice without a place reads row 0, and
+    // what it reads is not used.
+    __device__ __forceinline__ int64_t row(int j) const { return place[j] >= 0 ? place[j] : 0; }
+};
+
+// rows[position[t, j]] = x[t]: a token's row is read once and written to its places.
+// The grid's second axis cuts the columns into pieces of `span`.
+__global__ __launch_bounds__(256) void gather_kernel(Pairs p, int width, int lanes, int span,
+                                                     const int *__restrict__ position,
                                                      const float *__restrict__ x, int64_t ldx,
                                                      float *__restrict__ rows, int64_t ldrows) {
-    const int n = p.count();
-    for (int at = blockIdx.x; at < n; at += gridDim.x) {
-        const int f = order[at];
-        if (f < 0 || f >= n) continue;
-        const float *from = x + (int64_t)(f / p.top) * ldx;
-        float *to = rows + (int64_t)at * ldrows;
-        for (int c = threadIdx.x; c < width; c += 256) to[c] = from[c];
+    const int per = 256 / lanes, lane = threadIdx.x % lanes;
+    const int64_t t = (int64_t)blockIdx.x * per + threadIdx.x / lanes;
+    if (t >= p.tokens) return;
+    const int64_t begin = (int64_t)blockIdx.y * span, end = min((int64_t)width, begin + span);
+    for (int j0 = 0; j0 < p.top; j0 += J) {
+        const Choices k(p, t, j0, position, nullptr, 0);
+        for_columns(begin, end, lane, lanes, [&](int64_t c, auto vector) {
+            const auto v = load(x + t * ldx + c, vector);
+#pragma unroll
+            for (int j = 0; j < J; ++j)
+                if (k.place[j] >= 0) store(rows + k.place[j] * ldrows + c, v);
+        });
     }
 }
 
-// One work-group for each token in turn.
-__global__ __launch_bounds__(256) void combine_kernel(Pairs p, int width,
+// out[t] = sum of weights[t, j] * rows[position[t, j]] in the order of j.
+__global__ __launch_bounds__(256) void combine_kernel(Pairs p, int width, int lanes, int span,
                                                       const int *__restrict__ position,
                                                       const float *__restrict__ weights,
                                                       int64_t ldw, const float *__restrict__ rows,
                                                       int64_t ldrows, float *__restrict__ out,
                                                       int64_t ldout) {
-    const int n = p.count();
-    for (int t = blockIdx.x; t < p.tokens; t += gridDim.x) {
-        for (int c = threadIdx.x; c < width; c += 256) {
-            float sum = 0.0f;
-            for (int j = 0; j < p.top; ++j) {
-                const int at = position[(int64_t)t * p.top + j];
-                if (at < 0 || at >= n) continue;
-                const float w = weights ? weights[t * ldw + j] : 1.0f;
-                sum = fmaf(w, rows[at * ldrows + c], sum);
+    const int per = 256 / lanes, lane = threadIdx.x % lanes;
+    const int64_t t = (int64_t)blockIdx.x * per + threadIdx.x / lanes;
+    if (t >= p.tokens) return;
+    const int64_t begin = (int64_t)blockIdx.y * span, end = min((int64_t)width, begin + span);
+    const Choices first(p, t, 0, position, weights, ldw);
+    for_columns(begin, end, lane, lanes, [&](int64_t c, auto vector) {
+        Cols<decltype(vector)::value> sum = {};
+        auto add = [&](const Choices &k) {
+            Cols<decltype(vector)::value> v[J];
+#pragma unroll
+            for (int j = 0; j < J; ++j) v[j] = load(rows + k.row(j) * ldrows + c, vector);
+#pragma unroll
+            for (int j = 0; j < J; ++j)
+                if (k.place[j] >= 0) sum = mul_add(k.w[j], v[j], sum);
+        };
+        if (p.top > 0) add(first);
+        for (int j0 = J; j0 < p.top; j0 += J) add(Choices(p, t, j0, position, weights, ldw));
+        store(out + t * ldout + c, sum);
+    });
+}
+
+// The gradients of a token, four choices at a time: its dout is read once for them;
+// a choice's product with its row is added over the lanes in a fixed order (a
+// butterfly in each wave, then the waves in turn).
+__global__ __launch_bounds__(1024) void combine_grad_kernel(
+    Pairs p, int width, int lanes, const int *__restrict__ position,
+    const float *__restrict__ weights, int64_t ldw, const float *__restrict__ rows, int64_t ldrows,
+    const float *__restrict__ dout, int64_t lddout, float *__restrict__ drows, int64_t lddrows,
+    float *__restrict__ dweights) {
+    __shared__ float part[16][J];
+    const int per = blockDim.x / lanes, lane = threadIdx.x % lanes;
+    const int64_t token = (int64_t)blockIdx.x * per + threadIdx.x / lanes;
+    const bool have = token < p.tokens;  // every work-item reaches the barriers
+    const int64_t t = have ? token : 0;
+    for (int j0 = 0; j0 < p.top; j0 += J) {
+        const Choices k(p, t, j0, position, weights, ldw);
+        float dot[J] = {};
+        if (have) {
+            for_columns(0, width, lane, lanes, [&](int64_t c, auto vector) {
+                typedef Cols<decltype(vector)::value> V;
+                const V g = load(dout + t * lddout + c, vector);
+                if (dweights != nullptr) {
+                    V y[J];
+#pragma unroll
+                    for (int j = 0; j < J; ++j) y[j] = load(rows + k.row(j) * ldrows + c, vector);
+#pragma unroll
+                    for (int j = 0; j < J; ++j)
+                        if (k.place[j] >= 0) dot[j] = dot_add(g, y[j], dot[j]);
+                }
+                if (drows != nullptr) {
+#pragma unroll
+                    for (int j = 0; j < J; ++j)
+                        if (k.place[j] >= 0) store(drows + k.place[j] * lddrows + c, k.w[j] * g);
+                }
+            });
+        }
+        if (dweights == nullptr) continue;
+#pragma unroll
+        for (int j = 0; j < J; ++j)
+            for (int d = min(lanes, 64) / 2; d > 0; d /= 2) dot[j] += __shfl_xor(dot[j], d);
+        if (lanes > 64) {
+            const int wave = threadIdx.x >> 6;
+            __syncthreads();  // the last four choices' sums have been read
+            if ((threadIdx.x & 63) == 0) {
+#pragma unroll
+                for (int j = 0; j < J; ++j) part[wave][j] = dot[j];
             }
-            out[t * ldout + c] = sum;
+            __syncthreads();
+            if (lane == 0) {
+#pragma unroll
+                for (int j = 0; j < J; ++j)
+                    for (int i = 1; i < lanes / 64; ++i) dot[j] += part[wave + i][j];
+            }
+        }
+        if (have && lane == 0) {
+#pragma unroll
+            for (int j = 0; j < J; ++j)
+                if (j0 + j < p.top)
+                    dweights[t * ldw + j0 + j] = k.place[j] >= 0 ? dot[j] : 0.0f;
         }
     }
 }
 
-__global__ __launch_bounds__(256) void combine_grad_kernel(
-    Pairs p, int width, const int *__restrict__ position, const float *__restrict__ weights,
-    int64_t ldw, const float *__restrict__ rows, int64_t ldrows, const float *__restrict__ dout,
-    int64_t lddout, float *__restrict__ drows, int64_t lddrows, float *__restrict__ dweights) {
-    __shared__ float part[4];
-    const int n = p.count();
-    for (int f = blockIdx.x; f < n; f += gridDim.x) {
-        const int t = f / p.top, j = f % p.top, at = position[f];
-        const bool kept = at >= 0 && at < n;
-        const float w = weights ? weights[t * ldw + j] : 1.0f;
-        float dot = 0.0f;
-        if (kept)
-            for (int c = threadIdx.x; c < width; c += 256) {
-                const float g = dout[t * lddout + c];
-                if (drows) drows[at * lddrows + c] = w * g;
-                if (dweights) dot = fmaf(g, rows[at * ldrows + c], dot);
-            }
-        for (int d = 32; d; d /= 2) dot += __shfl_xor(dot, d);
-        if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = dot;
-        __syncthreads();
-        if (dweights && threadIdx.x == 0)
-            dweights[t * ldw + j] = ((part[0] + part[1]) + part[2]) + part[3];
-        __syncthreads();
-    }
+// Columns of a work-group's piece: all of them, or with too few tokens to fill the
+// chip pieces of one vector a lane.
+int span_for(int64_t groups, int width, int lanes) {
+    return groups >= 1024 ? width : 4 * lanes;
 }
-
-unsigned grid_for(int64_t groups) { return (unsigned)(groups < 65536 ? groups : 65536); }
 
 }  // namespace
 
-size_t route_workspace(Pairs, int) { return 0; }
-
-hipError_t launch_route_sort(Pairs p, int experts, const int *ids, int64_t ldids, int *offsets,
-                             int *order, int *position, void *, hipStream_t s) {
-    return launch(sort_kernel, dim3((unsigned)experts + 1), dim3(kSortThreads), 0, s, p, experts,
-                  ids, ldids, offsets, order, position);
+size_t route_workspace(Pairs p, int experts) {
+    int run, chunks;
+    sort_cut(p.count(), &run, &chunks);
+    return experts < kSortBuckets && chunks > 1 ? sizeof(int) * chunks * (size_t)(experts + 1) : 0;
 }
 
-hipError_t launch_route_gather(Pairs p, int width, const int *order, const float *x, int64_t ldx,
-                               float *rows, int64_t ldrows, hipStream_t s) {
-    return launch(gather_kernel, dim3(grid_for(p.count())), dim3(256), 0, s, p, width, order, x,
-                  ldx, rows, ldrows);
+hipError_t launch_route_sort(Pairs p, int experts, const int *ids, int64_t ldids, int *offsets,
+                             int *order, int *position, void *workspace, hipStream_t s) {
+    SortArgs a{p, experts, ids, ldids, 0, 0, (int *)workspace};
+    sort_cut(p.count(), &a.run, &a.chunks);
+    if (experts >= kSortBuckets)
+        return launch(sort_each_kernel, dim3((unsigned)experts + 1), dim3(kSortThreads), 0, s, a,
+                      offsets, order, position);
+    if (a.chunks == 1) {
+        a.counts = nullptr;
+    } else {
+        const hipError_t e = launch(sort_count_kernel, dim3((unsigned)a.chunks),
+                                    dim3(kSortThreads), 0, s, a);
+        if (e != hipSuccess) return e;
+    }
+    return launch(sort_place_kernel, dim3((unsigned)a.chunks), dim3(kSortThreads),
+                  sizeof(int) * kSortWaves * (size_t)(experts + 1), s, a, offsets, order,
+                  position);
+}
+
+hipError_t launch_route_gather(Pairs p, int width, const int *position, const float *x,
+                               int64_t ldx, float *rows, int64_t ldrows, hipStream_t s) {
+    const int lanes = lanes_for(width, 256);
+    const int64_t groups = ((int64_t)p.tokens * lanes + 255) / 256;
+    const int span = span_for(groups, width, lanes);
+    const dim3 grid((unsigned)groups, (unsigned)(((int64_t)width + span - 1) / span));
+    return launch(gather_kernel, grid, dim3(256), 0, s, p, width, lanes, span, position, x, ldx,
+                  rows, ldrows);
 }
 
 hipError_t launch_route_combine(Pairs p, int width, const int *position, const float *weights,
                                 int64_t ldw, const float *rows, int64_t ldrows, float *out,
                                 int64_t ldout, hipStream_t s) {
-    return launch(combine_kernel, dim3(grid_for(p.tokens)), dim3(256), 0, s, p, width, position,
-                  weights, ldw, rows, ldrows, out, ldout);
+    const int lanes = lanes_for(width, 256);
+    const int64_t groups = ((int64_t)p.tokens * lanes + 255) / 256;
+    const int span = span_for(groups, width, lanes);
+    const dim3 grid((unsigned)groups, (unsigned)(((int64_t)width + span - 1) / span));
+    return launch(combine_kernel, grid, dim3(256), 0, s, p, width, lanes, span, position, weights,
+                  ldw, rows, ldrows, out, ldout);
 }
 
 hipError_t launch_route_combine_grad(Pairs p, int width, const int *position,
@@ -145,8 +423,13 @@ hipError_t launch_route_combine_grad(Pairs p, int width, const int *position,
                                      int64_t ldrows, const float *dout, int64_t lddout,
                                      float *drows, int64_t lddrows, float *dweights,
                                      hipStream_t s) {
-    return launch(combine_grad_kernel, dim3(grid_for(p.count())), dim3(256), 0, s, p, width,
-                  position, weights, ldw, rows, ldrows, dout, lddout, drows, lddrows, dweights);
+    // with few tokens a row gets up to 1024 work-items
+    const int lanes = lanes_for(width, p.tokens < 512 ? 1024 : 256);
+    const int threads = lanes > 256 ? lanes : 256;
+    const int64_t groups = ((int64_t)p.tokens * lanes + threads - 1) / threads;
+    return launch(combine_grad_kernel, dim3((unsigned)groups), dim3((unsigned)threads), 0, s, p,
+                  width, lanes, position, weights, ldw, rows, ldrows, dout, lddout, drows,
+                  lddrows, dweights);
 }
 
 }  // namespace sgemm

@@ -82,14 +82,13 @@ def gather_rows(x, routing, out=None, stream=None):
     tokens, top = _pairs(routing)
     ldx = matrix(x, tokens, None, "x", device=routing.position.device)
     width = x.shape[1]
-    dense(routing.order, (tokens * top,), "routing.order", torch.int32, x.device)
     made = []
     if out is None:
         out = torch.empty((tokens * top, width), dtype=torch.float32, device=x.device)
         made.append(out)
     ldo = matrix(out, tokens * top, width, "out", device=x.device)
     call("sgemm_f32_route_gather", x.device, stream, made, tokens, top, width,
-         routing.order.data_ptr(), x.data_ptr(), ldx, out.data_ptr(), ldo)
+         routing.position.data_ptr(), x.data_ptr(), ldx, out.data_ptr(), ldo)
     return out
 
 

@@ -70,11 +70,11 @@ hipError_t sgemm_f32_route_sort(int tokens, int top, int experts,
                                 hipStream_t stream);
 
 /*
- * rows[p] = x[order[p] / top] for every place p < tokens*top with order[p] >= 0;
- * other rows are left as they are.  x is tokens x width (row stride ldx >=
- * max(1, width)), rows is tokens*top x width (ldrows >= max(1, width)).
+ * rows[position[f]] = x[f / top] for every pair f with a place; other rows are
+ * left as they are.  x is tokens x width (row stride ldx >= max(1, width)), rows is
+ * tokens*top x width (ldrows >= max(1, width)).
  */
-hipError_t sgemm_f32_route_gather(int tokens, int top, int width, const int *order,
+hipError_t sgemm_f32_route_gather(int tokens, int top, int width, const int *position,
                                   const float *x, int ldx,
                                   float *rows, int ldrows,
                                   hipStream_t stream);

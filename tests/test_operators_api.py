@@ -46,11 +46,11 @@ def test_sort_checks_its_workspace():
     assert sg.sgemm_f32_route_workspace_size(MAX, 2, 4) == 0
 
 
-GATHER = dict(tokens=8, top=2, width=16, order=A, x=B, ldx=16, rows=C, ldrows=16)
+GATHER = dict(tokens=8, top=2, width=16, position=A, x=B, ldx=16, rows=C, ldrows=16)
 
 
 @pytest.mark.parametrize("bad", [
-    dict(tokens=-1), dict(top=-1), dict(width=-1), dict(ldx=15), dict(ldrows=15), dict(order=0),
+    dict(tokens=-1), dict(top=-1), dict(width=-1), dict(ldx=15), dict(ldrows=15), dict(position=0),
     dict(x=0), dict(rows=0), dict(tokens=MAX, top=3), dict(rows=B + 64), dict(rows=A + 4)])
 def test_gather_refuses(bad):
     _refused("sgemm_f32_route_gather", GATHER, bad, GATHER)
@@ -180,7 +180,7 @@ def test_overlap_found_when_the_extent_passes_64_bits():
 
 
 def test_empty_calls_enqueue_nothing():
-    zero = {**GATHER, "tokens": 0, "order": 0, "x": 0, "rows": 0}
+    zero = {**GATHER, "tokens": 0, "position": 0, "x": 0, "rows": 0}
     assert sg.sgemm_f32_route_gather(*zero.values()) == 0
     zero = {**GATHER, "width": 0, "x": 0, "rows": 0}
     assert sg.sgemm_f32_route_gather(*zero.values()) == 0
