@@ -14,16 +14,20 @@ INT_MAX = 2**31 - 1
 
 def matrix(t, rows, cols, name, dtype=torch.float32, device=None):
     """The row stride of a rows x cols tensor with unit column stride (rows or cols
-    None: any number); raises where it is not one."""
-    if not isinstance(t, torch.Tensor) or t.dtype != dtype or t.dim() != 2:
+    None: any number) on GPU number `device` (None: any); raises where it is not
+    one."""
+    if not isinstance(t, torch.Tensor) or t.dtype is not dtype or t.dim() != 2:
         raise TypeError(f"{name} must be a 2-D {str(dtype).split('.')[-1]} torch tensor")
-    place(t, name, device)
+    if t.get_device() != device:
+        place(t, name, device)
     r, c = t.shape
     if (rows is not None and r != rows) or (cols is not None and c != cols):
         raise ValueError(f"{name} has the shape {r} x {c}; "
                          f"{'any' if rows is None else rows} x {'any' if cols is None else cols} "
                          "is needed")
     s0, s1 = t.stride()
+    if s1 == 1 and 0 < c <= s0 <= INT_MAX and 0 < r <= INT_MAX:
+        return s0
     if r == 0 or c == 0:
         return max(c, 1)
     if c > 1 and s1 != 1:
@@ -38,19 +42,24 @@ def matrix(t, rows, cols, name, dtype=torch.float32, device=None):
 
 
 def place(t, name, device):
-    """Raises unless t lives on the GPU (on `device`, if given)."""
-    if not t.is_cuda:
+    """The number of the GPU t lives on; raises unless it is on one (on `device`, if
+    given)."""
+    index = t.get_device()
+    if index < 0 or not t.is_cuda:
         raise ValueError(f"{name} must live on the GPU")
-    if device is not None and t.device != device:
-        raise ValueError(f"{name} lives on {t.device}, the other tensors on {device}")
+    if device is not None and index != device:
+        raise ValueError(f"{name} lives on GPU {index}, the other tensors on GPU {device}")
+    return index
 
 
 def dense(t, shape, name, dtype, device):
-    """Raises unless t is a contiguous tensor of this shape and type."""
-    if not isinstance(t, torch.Tensor) or t.dtype != dtype:
+    """Raises unless t is a contiguous tensor of this shape and type on GPU number
+    `device` (None: any)."""
+    if not isinstance(t, torch.Tensor) or t.dtype is not dtype:
         raise TypeError(f"{name} must be a {str(dtype).split('.')[-1]} torch tensor")
-    place(t, name, device)
-    if tuple(t.shape) != tuple(shape):
+    if t.get_device() != device:
+        place(t, name, device)
+    if t.shape != shape:
         raise ValueError(f"{name} has the shape {tuple(t.shape)}; {tuple(shape)} is needed")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
@@ -59,15 +68,14 @@ def dense(t, shape, name, dtype, device):
 _entries = {}   # library functions by name, looked up once
 
 
-def call(entry, device, stream, made, *args):
-    """entry(*args, stream) on the tensors' device, on `stream` (default: torch's
+def call(entry, index, stream, made, *args):
+    """entry(*args, stream) on GPU number `index`, on `stream` (default: torch's
     current stream there).  Tensors allocated for this call (`made`) are marked as
     used on a stream that is passed in, so that torch's allocator does not hand
     their memory out before the work there is done."""
     f = _entries.get(entry)
     if f is None:
         f = _entries[entry] = getattr(lib(), entry)
-    index = device.index
     if stream is not None:
         with torch.cuda.device(index):
             status = f(*args, stream.cuda_stream)

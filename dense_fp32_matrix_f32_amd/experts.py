@@ -33,13 +33,12 @@ class Routing(NamedTuple):
 
 
 def _pairs(routing):
-    """(tokens, top) of a routing, whose tensors are checked."""
+    """(tokens, top) of a routing, whose positions are checked."""
     position = routing.position
     if not isinstance(position, torch.Tensor) or position.dim() != 2:
         raise TypeError("routing.position must be a 2-D int32 torch tensor")
-    tokens, top = position.shape
-    dense(position, (tokens, top), "routing.position", torch.int32, None)
-    return tokens, top
+    dense(position, position.shape, "routing.position", torch.int32, None)
+    return position.shape
 
 
 def _offsets(offsets, device):
@@ -59,15 +58,15 @@ def sort_by_expert(ids, experts, stream=None):
     experts = int(experts)
     if tokens * top > INT_MAX or not 0 <= experts < INT_MAX:
         raise ValueError(f"{tokens} x {top} pairs for {experts} experts do not fit 32-bit numbers")
-    device = ids.device
-    offsets = torch.empty(experts + 1, dtype=torch.int32, device=device)
-    order = torch.empty(tokens * top, dtype=torch.int32, device=device)
-    position = torch.empty((tokens, top), dtype=torch.int32, device=device)
+    device = ids.get_device()
+    offsets = ids.new_empty(experts + 1)
+    order = ids.new_empty(tokens * top)
+    position = ids.new_empty((tokens, top))
     need = lib().sgemm_f32_route_workspace_size(tokens, top, experts)
     made = [offsets, order, position]
     workspace = None
     if need:
-        workspace = torch.empty(need, dtype=torch.uint8, device=device)
+        workspace = ids.new_empty(need // 4)
         made.append(workspace)
     call("sgemm_f32_route_sort", device, stream, made, tokens, top, experts, ids.data_ptr(), ld,
          offsets.data_ptr(), order.data_ptr(), position.data_ptr(),
@@ -80,14 +79,15 @@ def gather_rows(x, routing, out=None, stream=None):
     of the routing.  Rows past the last place are left as they are in ``out`` (and
     hold anything in a result allocated here)."""
     tokens, top = _pairs(routing)
-    ldx = matrix(x, tokens, None, "x", device=routing.position.device)
+    ldx = matrix(x, tokens, None, "x", device=routing.position.get_device())
     width = x.shape[1]
     made = []
     if out is None:
-        out = torch.empty((tokens * top, width), dtype=torch.float32, device=x.device)
+        out = x.new_empty((tokens * top, width))
         made.append(out)
-    ldo = matrix(out, tokens * top, width, "out", device=x.device)
-    call("sgemm_f32_route_gather", x.device, stream, made, tokens, top, width,
+    device = x.get_device()
+    ldo = matrix(out, tokens * top, width, "out", device=device)
+    call("sgemm_f32_route_gather", device, stream, made, tokens, top, width,
          routing.position.data_ptr(), x.data_ptr(), ldx, out.data_ptr(), ldo)
     return out
 
@@ -97,13 +97,13 @@ def combine_rows(rows, routing, weights=None, out=None, stream=None):
     its choices: tokens x width.  Dropped pairs add nothing.  Without weights this is
     the gradient of gather_rows."""
     tokens, top = _pairs(routing)
-    device = routing.position.device
+    device = routing.position.get_device()
     ldr = matrix(rows, tokens * top, None, "rows", device=device)
     width = rows.shape[1]
     ldw = 1 if weights is None else matrix(weights, tokens, top, "weights", device=device)
     made = []
     if out is None:
-        out = torch.empty((tokens, width), dtype=torch.float32, device=device)
+        out = rows.new_empty((tokens, width))
         made.append(out)
     ldo = matrix(out, tokens, width, "out", device=device)
     call("sgemm_f32_route_combine", device, stream, made, tokens, top, width,
@@ -118,7 +118,7 @@ def combine_rows_grad(dout, rows, routing, weights=None, drows=None, stream=None
     last place are left as they are in ``drows`` (and hold anything in a tensor
     allocated here)."""
     tokens, top = _pairs(routing)
-    device = routing.position.device
+    device = routing.position.get_device()
     ldd = matrix(dout, tokens, None, "dout", device=device)
     width = dout.shape[1]
     ldr = matrix(rows, tokens * top, width, "rows", device=device)
@@ -127,12 +127,12 @@ def combine_rows_grad(dout, rows, routing, weights=None, drows=None, stream=None
     if weights is not None:
         ldw = matrix(weights, tokens, top, "weights", device=device)
         if ldw == max(top, 1):
-            dweights = torch.empty((tokens, top), dtype=torch.float32, device=device)
+            dweights = weights.new_empty((tokens, top))
         else:  # the library gives the gradient the weights' row stride
-            dweights = torch.empty((tokens, ldw), dtype=torch.float32, device=device)[:, :top]
+            dweights = weights.new_empty((tokens, ldw))[:, :top]
         made.append(dweights)
     if drows is None:
-        drows = torch.empty((tokens * top, width), dtype=torch.float32, device=device)
+        drows = rows.new_empty((tokens * top, width))
         made.append(drows)
     lddr = matrix(drows, tokens * top, width, "drows", device=device)
     call("sgemm_f32_route_combine_grad", device, stream, made, tokens, top, width,
@@ -147,7 +147,8 @@ def _stack(B, name, device):
     cols tensor whose matrices are row-major or transposes of row-major ones."""
     if not isinstance(B, torch.Tensor) or B.dtype != torch.float32 or B.dim() != 3:
         raise TypeError(f"{name} must be a 3-D float32 torch tensor")
-    place(B, name, device)
+    if B.get_device() != device:
+        place(B, name, device)
     e, r, c = B.shape
     se, s0, s1 = B.stride()
     if e == 0 or r == 0 or c == 0:
@@ -171,7 +172,7 @@ def grouped_matmul(A, B, offsets, out=None, alpha=1.0, beta=0.0, stream=None):
     expanded first dimension as one shared matrix.  Rows of no expert are left as
     they are in ``out`` (and hold anything in a result allocated here)."""
     lda = matrix(A, None, None, "A")
-    device = A.device
+    device = A.get_device()
     rows, K = A.shape
     ldb, strideb, trans = _stack(B, "B", device)
     experts, K2, N = B.shape
@@ -183,7 +184,7 @@ def grouped_matmul(A, B, offsets, out=None, alpha=1.0, beta=0.0, stream=None):
     if out is None:
         if beta != 0.0:
             raise ValueError("beta != 0 needs out")
-        out = torch.empty((rows, N), dtype=torch.float32, device=device)
+        out = A.new_empty((rows, N))
         made.append(out)
     ldc = matrix(out, rows, N, "out", device=device)
     call("sgemm_f32_grouped", device, stream, made, int(trans), rows, N, K, experts,
@@ -198,7 +199,7 @@ def grouped_matmul_ta(A, D, offsets, out=None, alpha=1.0, beta=0.0, stream=None)
     the gradient of grouped_matmul(A, B, offsets) with respect to B for D = the
     gradient of its result.  An expert without rows gets zeros (beta * out[e])."""
     lda = matrix(A, None, None, "A")
-    device = A.device
+    device = A.get_device()
     rows, M = A.shape
     ldd = matrix(D, rows, None, "D", device=device)
     N = D.shape[1]
@@ -207,7 +208,7 @@ def grouped_matmul_ta(A, D, offsets, out=None, alpha=1.0, beta=0.0, stream=None)
     if out is None:
         if beta != 0.0:
             raise ValueError("beta != 0 needs out")
-        out = torch.empty((experts, M, N), dtype=torch.float32, device=device)
+        out = A.new_empty((experts, M, N))
         made.append(out)
     elif tuple(out.shape) != (experts, M, N):
         raise ValueError("out has the wrong shape")

@@ -65,11 +65,11 @@ def w4_pack(codes, scales, zeros=None, *, K, group, stream=None):
     dense(codes, lead + (-(-K // 2), N), "codes", torch.uint8, None)
     if not isinstance(scales, torch.Tensor) or scales.dtype not in SCALE_TYPES:
         raise TypeError("scales must be a float32, float16 or bfloat16 torch tensor")
-    dense(scales, lead + (groups, N), "scales", scales.dtype, codes.device)
+    dense(scales, lead + (groups, N), "scales", scales.dtype, codes.get_device())
     if zeros is not None:
-        dense(zeros, lead + (groups, N), "zeros", torch.uint8, codes.device)
+        dense(zeros, lead + (groups, N), "zeros", torch.uint8, codes.get_device())
     w = _new(experts, stacked, K, N, group, scales.dtype, zeros is not None, codes.device)
-    call("sgemm_f32_w4_pack", codes.device, stream, [w.packed], experts, N, K, group,
+    call("sgemm_f32_w4_pack", codes.get_device(), stream, [w.packed], experts, N, K, group,
          codes.data_ptr(), scales.data_ptr(), w.scale_type,
          0 if zeros is None else zeros.data_ptr(), w.packed.data_ptr(), w.packed.numel())
     return w
@@ -88,7 +88,7 @@ def w4_quantize(B, group=128, zeros=False, scale_dtype=torch.float32, stream=Non
         raise ValueError("B must hold row-major matrices")
     experts, K, N = stack.shape
     w = _new(experts, stacked, K, N, group, scale_dtype, zeros, B.device)
-    call("sgemm_f32_w4_quantize", B.device, stream, [w.packed], experts, N, K, group,
+    call("sgemm_f32_w4_quantize", B.get_device(), stream, [w.packed], experts, N, K, group,
          B.data_ptr(), ldb, strideb, w.scale_type, int(w.zeros), w.packed.data_ptr(),
          w.packed.numel())
     return w
@@ -96,8 +96,8 @@ def w4_quantize(B, group=128, zeros=False, scale_dtype=torch.float32, stream=Non
 
 def w4_unpack(w, stream=None):
     """The float32 matrices that w stands for, [experts x] K x N."""
-    device = w.packed.device
-    out = torch.empty((w.experts, w.K, w.N), dtype=torch.float32, device=device)
+    device = w.packed.get_device()
+    out = torch.empty((w.experts, w.K, w.N), dtype=torch.float32, device=w.packed.device)
     call("sgemm_f32_w4_unpack", device, stream, [out], w.experts, w.N, w.K, w.group, w.scale_type,
          int(w.zeros), w.packed.data_ptr(), w.packed.numel(), out.data_ptr(), max(w.N, 1),
          w.K * w.N)
@@ -109,8 +109,8 @@ def matmul_w4(A, w, offsets=None, out=None, stream=None):
     (int32, experts + 1 values) row i times the matrix of its expert e, offsets[e] <=
     i < offsets[e+1].  Rows of no expert are left as they are in ``out`` (and hold
     anything in a result allocated here)."""
-    lda = matrix(A, None, w.K, "A", device=w.packed.device)
-    device = A.device
+    lda = matrix(A, None, w.K, "A", device=w.packed.get_device())
+    device = A.get_device()
     rows = A.shape[0]
     if offsets is None:
         if w.experts != 1:
@@ -119,7 +119,7 @@ def matmul_w4(A, w, offsets=None, out=None, stream=None):
         raise ValueError(f"{offsets.numel()} offsets for {w.experts} experts")
     made = []
     if out is None:
-        out = torch.empty((rows, w.N), dtype=torch.float32, device=device)
+        out = A.new_empty((rows, w.N))
         made.append(out)
     ldc = matrix(out, rows, w.N, "out", device=device)
     if offsets is None:
