@@ -4,9 +4,11 @@
 // A matrix is cut into strips of 16 columns and each strip into blocks of 128 k.
 // A block is one record: 1024 bytes of codes, then its scales, then its zero
 // points (if any).  The 16 bytes at 16*lane belong to column lane % 16; word j of
-// them holds the codes of k = 32*j + 8*(lane / 16) + i, i = 0 .. 7, so one
-// 16-byte load a lane fetches a block and its word j is the lane's operand of the
-// j-th 16x16x32 matrix instruction.  Within a word, codes 0 .. 3 are the low
+// them holds the codes of k = 32*j + 4*q + 0 .. 3 and 32*j + 16 + 4*q + 0 .. 3, q =
+// lane / 16, so one 16-byte load a lane fetches a block and its word j is the lane's
+// operand of the j-th 16x16x32 matrix instruction (which adds over k in any order that
+// both operands share; in this one the lanes of a row of A load 64 bytes side by
+// side).  Within a word, codes 0 .. 3 are the low
 // halves of bytes 0 .. 3 and codes 4 .. 7 their high halves: two masks give
 // eight bytes, each the code itself.  Scales and zero points are [column][part]
 // with one part for each min(group, 128) values of k, so a lane fetches those of
@@ -69,6 +71,11 @@ __device__ __forceinline__ float w4_store_scale(unsigned char *p, float x, int s
     }
     return w4_scale(p, scale_type);
 }
+
+// k of code i of lane part q within its 32 k, and back.
+__host__ __device__ constexpr int w4_k(int q, int i) { return 16 * (i / 4) + 4 * q + i % 4; }
+__host__ __device__ constexpr int w4_part(int k) { return k % 16 / 4; }
+__host__ __device__ constexpr int w4_index(int k) { return 4 * (k / 16) + k % 4; }
 
 // Place of code i of a word.
 __host__ __device__ constexpr int w4_shift(int i) { return i < 4 ? 8 * i : 8 * (i - 4) + 4; }

@@ -66,6 +66,21 @@ __device__ __forceinline__ float lower(float x) {
     return x - __builtin_bit_cast(float, bits(x) & 0xFFFF0000u);
 }
 
+// The lane that cuts k = 4*(lane % 32) .. +3 of a block writes one half of a run: the
+// run of lane part q of step j, 4*j + q, holds the eight k that w4_k(q, ..) names.
+__device__ __forceinline__ int run_of(int lane) {
+    const int k = 4 * (lane & 31);
+    return k / 32 * 4 + w4_part(k % 32);
+}
+__device__ __forceinline__ int half_of(int lane) { return w4_index(4 * (lane & 31) % 32) / 4; }
+
+// LDS holds, for each run of 8 k, 16-byte slots of the instruction rows.  Within each
+// 16 rows a row's slot is permuted by the run's number: the writers of one row (two
+// lanes a run) then fill all 64 banks once, and so do the lanes that a 16-byte read
+// serves in one cycle (with a padded pitch instead, two fifths of the LDS cycles of
+// the kernel for many rows were conflicts).
+__device__ __forceinline__ int slot_of(int row, int run) { return row ^ run; }
+
 // Writes by some lanes of a wave are read by others of the same wave.
 __device__ __forceinline__ void wave_sync() {
     __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
@@ -74,11 +89,14 @@ __device__ __forceinline__ void wave_sync() {
 }
 
 // How a work-group's MR rows of A meet the matrix instructions of 16 rows.  A lane
-// loads XV float4 vectors of A for a block of 128 k, two rows at a time.
+// loads XV float4 vectors of A for a block of 128 k.
 //   few rows: the three parts of row m are instruction rows 3m .. 3m+2, so 2 or 5
-//   rows take one instruction and 10 take two; the parts' sums are added at the end;
+//   rows take one instruction and 10 take two; the parts' sums are added at the end.
+//   A wave loads two rows at a time and hands the parts to the lanes that need them
+//   through LDS;
 //   16 rows:  each part is an instruction of its own and all three add into the
-//   same registers, which leaves a third of the registers and of the scaling.
+//   same registers, which leaves a third of the registers and of the scaling.  A lane
+//   loads the values that it needs itself and cuts them in registers.
 template <int XV_>
 struct Rows {
     static constexpr int XV = XV_;
@@ -86,7 +104,6 @@ struct Rows {
     static constexpr bool ADD = MR == 16;
     static constexpr int AT = (3 * MR + 15) / 16;  // operands of 16 rows
     static constexpr int RT = ADD ? 1 : AT;        // results of 16 rows
-    static constexpr int ROW = ADD ? 1 : 3, PART = ADD ? 16 : 1;  // place of row m, part p
 };
 
 // Where a lane finds its share of a record.  The loads take no branch on the type
@@ -175,6 +192,21 @@ __device__ __forceinline__ void store_parts(f32x4 x, unsigned char *p0, unsigned
     *(uint2 *)p2 = uint2{upper(z[0], z[1]), upper(z[2], z[3])};
 }
 
+// Eight values of a row of A as the operands of its three parts.
+__device__ __forceinline__ void cut_parts(f32x4 lo, f32x4 hi, bf16x8 (&a)[3]) {
+#pragma unroll
+    for (int part = 0; part < 3; ++part) {
+        const Frag f{.word = {upper(lo[0], lo[1]), upper(lo[2], lo[3]), upper(hi[0], hi[1]),
+                              upper(hi[2], hi[3])}};
+        a[part] = f.v;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            lo[e] = lower(lo[e]);
+            hi[e] = lower(hi[e]);
+        }
+    }
+}
+
 // The value of the lane whose number differs in bit D (1, 2 or 4).
 template <int D>
 __device__ __forceinline__ float lane_xor(float x) {
@@ -190,15 +222,17 @@ __device__ __forceinline__ float lane_xor(float x) {
     }
 }
 
-// W waves, R rows, CT strips of columns, PARTS scales of a column in a block, the
-// loads of D blocks in flight in each wave.
-template <int W, class R, int CT, int PARTS, int D>
+// R rows, CT strips of columns, PARTS scales of a column in a block, the loads of D
+// blocks in flight in each wave.
+constexpr int W = 8;  // waves
+
+template <class R, int CT, int PARTS, int D>
 __global__ __launch_bounds__(W * 64) void w4_kernel(W4Layout l, W4Problem p, int row_blocks) {
     constexpr int MR = R::MR, RT = R::RT, AT = R::AT, XV = R::XV;
-    constexpr int RP = 16 * AT + 1;   // 16-byte slots of one run of 8 k in LDS
+    constexpr int RP = 16 * AT;       // 16-byte slots of one run of 8 k in LDS
     constexpr int STEPS = 4 / PARTS;  // matrix instructions of 32 k under one scale
     constexpr int COLS = kW4Cols * CT;
-    constexpr int XS = 16 * RP * 16;               // bytes of a wave's parts of A
+    constexpr int XS = R::ADD ? 0 : 16 * RP * 16;  // bytes of a wave's parts of A
     constexpr int RED = 16 * RT * (COLS + 1) * 4;  // bytes of a wave's sums
     __shared__ __attribute__((aligned(16))) unsigned char lds[W * (XS > RED ? XS : RED)];
 
@@ -219,11 +253,16 @@ __global__ __launch_bounds__(W * 64) void w4_kernel(W4Layout l, W4Problem p, int
     for (int c = 0; c < CT; ++c)
         strip[c] = p.packed + expert * l.expert_bytes +
                    min(strip0 + c, l.strips - 1) * l.strip_bytes;
-    const float *arow[XV];
+    // vector i of this lane: four k from k_of(i) of a block on, of row arow[i]
+    constexpr int AROWS = R::ADD ? 1 : XV;
+    const float *arow[AROWS];
 #pragma unroll
-    for (int i = 0; i < XV; ++i)
-        arow[i] = p.A + (int64_t)(first + min(2 * i + (lane >> 5), rows - 1)) * p.lda;
-    const int k_lane = 4 * (lane & 31);
+    for (int i = 0; i < AROWS; ++i)
+        arow[i] = p.A + (int64_t)(first + min(R::ADD ? lane & 15 : 2 * i + (lane >> 5), rows - 1)) *
+                            p.lda;
+    auto k_of = [&](int i) {
+        return R::ADD ? 32 * (i / 2) + w4_k(lane >> 4, 4 * (i % 2)) : 4 * (lane & 31);
+    };
 
     // One block of 128 k in registers.
     struct Block {
@@ -235,13 +274,19 @@ __global__ __launch_bounds__(W * 64) void w4_kernel(W4Layout l, W4Problem p, int
 #pragma unroll
         for (int c = 0; c < CT; ++c) b.w[c].load(strip[c] + (int64_t)block * l.record, at);
 #pragma unroll
-        for (int i = 0; i < XV; ++i) b.x[i] = load_k(arow[i], block * kW4Block + k_lane, l.K);
+        for (int i = 0; i < XV; ++i)
+            b.x[i] = load_k(arow[R::ADD ? 0 : i], block * kW4Block + k_of(i), l.K);
     };
 
+    // in LDS: this lane's four k of row 2i + lane/32, and its operand of step j
     unsigned char *xs = lds + wave * XS;
-    // place of this lane's four k of row 2i + lane/32; of its operand
-    unsigned char *put = xs + (((lane & 31) >> 1) * RP + R::ROW * (lane >> 5)) * 16 + (lane & 1) * 8;
-    const unsigned char *get = xs + ((lane >> 4) * RP + (lane & 15)) * 16;
+    const int put_run = run_of(lane);
+    unsigned char *put = xs + put_run * RP * 16 + half_of(lane) * 8;
+    auto put_at = [&](int row) { return put + slot_of(row, put_run) * 16; };
+    auto get = [&](int j, int r) {
+        const int run = 4 * j + (lane >> 4);
+        return *(const bf16x8 *)(xs + (run * RP + slot_of(lane & 15, run) + 16 * r) * 16);
+    };
 
     f32x4 total[RT][CT];
 #pragma unroll
@@ -255,15 +300,17 @@ __global__ __launch_bounds__(W * 64) void w4_kernel(W4Layout l, W4Problem p, int
         if (block * kW4Block + kW4Block > l.K) {
 #pragma unroll
             for (int i = 0; i < XV; ++i)
-                b.x[i] = last_k(b.x[i], block * kW4Block + k_lane, l.K);
+                b.x[i] = last_k(b.x[i], block * kW4Block + k_of(i), l.K);
         }
+        if constexpr (!R::ADD) {
 #pragma unroll
-        for (int i = 0; i < XV; ++i) {
-            if (2 * i + 1 >= MR && (lane >> 5)) continue;
-            unsigned char *to = put + 2 * i * R::ROW * 16;
-            store_parts(b.x[i], to, to + 16 * R::PART, to + 32 * R::PART);
+            for (int i = 0; i < XV; ++i) {
+                if (2 * i + 1 >= MR && (lane >> 5)) continue;
+                const int row = 3 * (2 * i + (lane >> 5));
+                store_parts(b.x[i], put_at(row), put_at(row + 1), put_at(row + 2));
+            }
+            wave_sync();
         }
-        wave_sync();
 #pragma unroll
         for (int t = 0; t < PARTS; ++t) {
             // column c < CT; sums of A in column CT
@@ -272,9 +319,12 @@ __global__ __launch_bounds__(W * 64) void w4_kernel(W4Layout l, W4Problem p, int
             for (int u = 0; u < STEPS; ++u) {
                 const int j = t * STEPS + u;
                 bf16x8 a[AT], q[CT + 1];
+                if constexpr (R::ADD) {
+                    cut_parts(b.x[2 * j], b.x[2 * j + 1], a);
+                } else {
 #pragma unroll
-                for (int r = 0; r < AT; ++r)
-                    a[r] = *(const bf16x8 *)(get + (4 * j * RP + 16 * r) * 16);
+                    for (int r = 0; r < AT; ++r) a[r] = get(j, r);
+                }
 #pragma unroll
                 for (int c = 0; c < CT; ++c) q[c] = codes_of(b.w[c].word(j));
                 q[CT] = ones.v;
@@ -300,7 +350,7 @@ __global__ __launch_bounds__(W * 64) void w4_kernel(W4Layout l, W4Problem p, int
             }
             __builtin_amdgcn_sched_barrier(0);
         }
-        wave_sync();
+        if constexpr (!R::ADD) wave_sync();
     };
 
     // Blocks wave, wave + W, ...: the loads of the next D are always issued before
@@ -343,12 +393,12 @@ __global__ __launch_bounds__(W * 64) void w4_kernel(W4Layout l, W4Problem p, int
         for (int part = R::ADD ? 0 : 2; part >= 0; --part)
 #pragma unroll
             for (int w = 0; w < W; ++w)
-                sum += red[(w * 16 * RT + R::ROW * m + part) * (COLS + 1) + col];
+                sum += red[(w * 16 * RT + (R::ADD ? m : 3 * m + part)) * (COLS + 1) + col];
         p.C[(int64_t)(first + m) * p.ldc + n_at] = sum;
     }
 }
 
-template <int W, class R, int CT, int D>
+template <class R, int CT, int D>
 hipError_t launch_rows(const W4Layout &l, const W4Problem &p, hipStream_t s) {
     const int64_t row_blocks = p.offsets != nullptr ? most_blocks(p.rows, p.experts, R::MR)
                                                     : ((int64_t)p.rows + R::MR - 1) / R::MR;
@@ -356,16 +406,16 @@ hipError_t launch_rows(const W4Layout &l, const W4Problem &p, hipStream_t s) {
     if (groups > INT32_MAX) return hipErrorInvalidValue;
     const dim3 grid((unsigned)groups), block(W * 64);
     switch (l.parts) {
-    case 4: return launch(w4_kernel<W, R, CT, 4, D>, grid, block, 0, s, l, p, (int)row_blocks);
-    case 2: return launch(w4_kernel<W, R, CT, 2, D>, grid, block, 0, s, l, p, (int)row_blocks);
-    default: return launch(w4_kernel<W, R, CT, 1, D>, grid, block, 0, s, l, p, (int)row_blocks);
+    case 4: return launch(w4_kernel<R, CT, 4, D>, grid, block, 0, s, l, p, (int)row_blocks);
+    case 2: return launch(w4_kernel<R, CT, 2, D>, grid, block, 0, s, l, p, (int)row_blocks);
+    default: return launch(w4_kernel<R, CT, 1, D>, grid, block, 0, s, l, p, (int)row_blocks);
     }
 }
 
 // ---------------------------------------------------------------------------
 // Many rows.  Cutting A into parts costs about six vector operations a value, and
 // in the kernel above every work-group cuts its rows for 16 to 64 columns only.
-// Here a work-group computes BM rows by 256 columns over all k, its waves side by
+// Here a work-group computes BM rows by 256 or 512 columns over all k, its waves side by
 // side in columns, and A is cut once for all of them, into two stages of LDS: while
 // one block of 128 k is multiplied, the next one's x is cut, one barrier a block.
 // The sums of A over 32 k (for the zero points) are formed on the way, in fp32.
@@ -374,7 +424,7 @@ struct Wide {
     static constexpr int D = D_;  // blocks of 128 k whose loads are in flight (even)
     static constexpr int RTW = RTW_, CTW = CTW_;  // 16-row and 16-column tiles of a wave
     static constexpr int BM = 16 * RTW, STRIPS = W_ * CTW, THREADS = 64 * W_;
-    static constexpr int RP = 3 * BM + 1;  // 16-byte slots of one run of 8 k in LDS
+    static constexpr int RP = 3 * BM;  // 16-byte slots of one run of 8 k in LDS
     static constexpr int XV = BM * 32 / THREADS;  // float4 vectors of A a lane and step
     static_assert(BM * 32 % THREADS == 0, "whole vectors");
 };
@@ -433,8 +483,8 @@ __global__ __launch_bounds__(T::THREADS) void w4_wide_kernel(W4Layout l, W4Probl
         }
     };
     auto cut = [&](f32x4 x, int v, int stage) {
-        unsigned char *to =
-            xs[stage] + (((tid & 31) >> 1) * RP + tid / 32 + v * VROWS) * 16 + (tid & 1) * 8;
+        const int run = run_of(tid), row = tid / 32 + v * VROWS;
+        unsigned char *to = xs[stage] + (run * RP + slot_of(row, run)) * 16 + half_of(tid) * 8;
         store_parts(x, to, to + BM * 16, to + 2 * BM * 16);
         // eight lanes hold 32 k of a row
         float t = (x[0] + x[1]) + (x[2] + x[3]);
@@ -453,8 +503,11 @@ __global__ __launch_bounds__(T::THREADS) void w4_wide_kernel(W4Layout l, W4Probl
     // The products of one block, in LDS stage `stage`, and between them the cutting of
     // the next block's x into the other stage.
     auto multiply = [&](const Block &b, const f32x4(&x)[XV], int stage) {
-        const unsigned char *get =
-            xs[stage] + ((lane >> 4) * RP + (lane & 15)) * 16;
+        auto get = [&](int j, int row) {
+            const int run = 4 * j + (lane >> 4);
+            return *(const bf16x8 *)(xs[stage] +
+                                     (run * RP + slot_of(lane & 15, run) + row) * 16);
+        };
 #pragma unroll
         for (int t = 0; t < PARTS; ++t) {
             f32x4 sum[RTW][CTW];
@@ -466,10 +519,13 @@ __global__ __launch_bounds__(T::THREADS) void w4_wide_kernel(W4Layout l, W4Probl
                 for (int r = 0; r < RTW; ++r)
 #pragma unroll
                     for (int part = 2; part >= 0; --part)
-                        a[r][part] =
-                            *(const bf16x8 *)(get + (4 * j * RP + part * BM + 16 * r) * 16);
+                        a[r][part] = get(j, part * BM + 16 * r);
 #pragma unroll
                 for (int c = 0; c < CTW; ++c) q[c] = codes_of(b.w[c].word(j));
+                // a wave in its matrix instructions goes first, so that the other waves of
+                // its SIMD unpack and cut in their shadow
+                __builtin_amdgcn_sched_barrier(0);
+                __builtin_amdgcn_s_setprio(1);
 #pragma unroll
                 for (int part = 2; part >= 0; --part)
 #pragma unroll
@@ -479,6 +535,8 @@ __global__ __launch_bounds__(T::THREADS) void w4_wide_kernel(W4Layout l, W4Probl
                             sum[r][c] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
                                 a[r][part], q[c], u == 0 && part == 2 ? f32x4{} : sum[r][c], 0, 0,
                                 0);
+                __builtin_amdgcn_s_setprio(0);
+                __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
                 for (int v = j * XV / 4; v < (j + 1) * XV / 4; ++v) cut(x[v], v, 1 - stage);
             }
@@ -567,7 +625,8 @@ __global__ __launch_bounds__(256) void w4_short_kernel(W4Layout l, W4Problem p) 
             const float s = w4_scale(rec + kW4Codes + part * l.scale_size, l.scale_type);
             const int z = l.zeros ? rec[kW4Codes + l.parts * kW4Cols * l.scale_size + part] : 8;
             for (int k = 0; k < l.K; ++k)
-                sum = fmaf(p.A[row * p.lda + k], (float)((int)(word >> w4_shift(k) & 15) - z), sum);
+                sum = fmaf(p.A[row * p.lda + k],
+                           (float)((int)(word >> w4_shift(w4_index(k)) & 15) - z), sum);
             sum *= s;
         }
         p.C[row * p.ldc + n] = sum;
@@ -592,16 +651,29 @@ bool wide_fits(const W4Layout &l, const W4Problem &p) {
     return (T::BM - 1) * p.lda + l.K < ((int64_t)1 << 32);
 }
 
-template <class T>
+template <class T, int PARTS>
 hipError_t launch_wide(const W4Layout &l, const W4Problem &p, hipStream_t s) {
     const int64_t groups = wide_groups<T>(l, p);
     if (groups > INT32_MAX) return hipErrorInvalidValue;
-    const dim3 grid((unsigned)groups), block(T::THREADS);
-    const int row_blocks = (int)wide_blocks<T>(p);
+    return launch(w4_wide_kernel<T, PARTS>, dim3((unsigned)groups), dim3(T::THREADS), 0, s, l, p,
+                  (int)wide_blocks<T>(p));
+}
+
+// 32 rows by 256 or 512 columns.  The wider block halves the cutting of A and the
+// reads of its parts from LDS; it is taken where it still gives every CU a
+// work-group, and not with four scales of a column in a block, which need more
+// registers than it leaves (512 rows 8192 x 4096, group 128: 90.4 against 94.4 us;
+// 2048 rows 4096 x 4096, group 64: 191 against 225; 512 rows 4096 x 4096, group 32:
+// 252 against 67).
+using Wide256 = Wide<8, 2, 2, 2>;
+using Wide512 = Wide<8, 2, 4, 2>;
+
+hipError_t launch_many_rows(const W4Layout &l, const W4Problem &p, hipStream_t s) {
+    const bool wider = wide_groups<Wide512>(l, p) >= compute_units();
     switch (l.parts) {
-    case 4: return launch(w4_wide_kernel<T, 4>, grid, block, 0, s, l, p, row_blocks);
-    case 2: return launch(w4_wide_kernel<T, 2>, grid, block, 0, s, l, p, row_blocks);
-    default: return launch(w4_wide_kernel<T, 1>, grid, block, 0, s, l, p, row_blocks);
+    case 4: return launch_wide<Wide256, 4>(l, p, s);
+    case 2: return wider ? launch_wide<Wide512, 2>(l, p, s) : launch_wide<Wide256, 2>(l, p, s);
+    default: return wider ? launch_wide<Wide512, 1>(l, p, s) : launch_wide<Wide256, 1>(l, p, s);
     }
 }
 
@@ -609,21 +681,24 @@ hipError_t launch_wide(const W4Layout &l, const W4Problem &p, hipStream_t s) {
 
 // The kernel for a call, by the rows that share a reading of the weights (for
 // experts, if each had the same number) and the strips.  Times in us, back to back,
-// weights of three calls in turn (8.7 MB for 4096 x 4096):
+// random data, the weights of three calls in turn (8.7 MB for 4096 x 4096):
 //   rows  N x K, group      choice           others
-//   1     4096 x 4096, 128  8 waves 4.2      16 waves 4.3, 4 waves 5.0, two strips 5.2
-//   1     8192 x 8192, 128  one strip 9.1    two strips 9.1
-//   8 by expert, 64 x 2048 x 2048: two strips 6.8, one 7.5
-//   5     4096 x 4096, 64   16 waves 5.1     8 waves 5.5
-//   8     4096 x 4096, 128  16 waves 6.2     8 waves 6.3; 16-row form 8.2
-//   16    4096 x 4096, 128  one strip 8.2    two 9.3, four 12.0
-//   16    8192 x 8192, 64   two strips 17.9  one 27.9, four 23.7
-//   64    4096 x 4096, 128  four strips 13.0 two 18.3, one 28.7; many-rows form 51
-//   128   4096 x 4096, 64   four strips 25.7 two 36.0; many-rows form 54
-//   512   4096 x 4096, 32   many rows 64.9   four strips 114
-//   512   8192 x 4096, 128  many rows 85.4   four strips 194
-// Slices of k over several work-groups, their sums added by a second kernel, brought
-// 16 x 8192 x 8192 to 17.0 and 128 x 4096 x 4096 to 24.1 us and were not kept.
+//   1     4096 x 4096, 128  one strip 4.5    two 5.3; 4 waves 5.3, 16 waves 4.6
+//   1     8192 x 8192, 128  one strip 9.5    two 9.4; 4 waves 10.2, 16 waves 9.5
+//   8 by expert, 64 x 2048 x 2048, 128: two strips 6.8, one 8.1
+//   5     4096 x 4096, 64   5-row form 5.5   10-row form 6.9
+//   8     4096 x 4096, 128  10-row form 6.8  16-row form 7.9
+//   16    4096 x 4096, 128  one strip 9.7    two 10.2, four 13.0; 10-row form 9.7
+//   16    8192 x 8192, 64   two strips 19.1  one 32.8, four 24.6
+//   32    4096 x 4096, 128  two strips 10.6  one 17.2, four 13.5
+//   256 by expert, 16 x 1408 x 4096, 32: two strips 38.8, one 58, four 44
+//   64    4096 x 4096, 128  four strips 14.1 two 18.9; many-rows form 50
+//   128   4096 x 4096, 64   four strips 27.0 two 35.2; many-rows form 54
+//   512   4096 x 4096, 32   many rows 65     four strips 121
+//   512   8192 x 4096, 128  many rows 88     four strips 197
+// (4.5 us is 1.9 TB/s; a kernel that does nothing takes about 2.5.)  Slices of k over
+// several work-groups, their sums added by a second kernel, brought 16 x 8192 x 8192
+// from 17.9 to 17.0 us and were not kept.
 hipError_t launch_w4(const W4Layout &l, const W4Problem &p, hipStream_t s) {
     if (l.K < 4) {
         const dim3 grid((unsigned)((l.N + 255ll) / 256),
@@ -634,18 +709,17 @@ hipError_t launch_w4(const W4Layout &l, const W4Problem &p, hipStream_t s) {
     const int64_t each = ((int64_t)p.rows + experts - 1) / experts;
     if (each <= 2) {
         const int64_t groups = l.strips * (p.offsets != nullptr ? most_blocks(p.rows, experts, 2) : 1);
-        return groups >= 1024 ? launch_rows<8, Rows<1>, 2, 2>(l, p, s)
-                              : launch_rows<8, Rows<1>, 1, 2>(l, p, s);
+        return groups >= 1024 ? launch_rows<Rows<1>, 2, 2>(l, p, s)
+                              : launch_rows<Rows<1>, 1, 2>(l, p, s);
     }
-    if (each <= 5) return launch_rows<16, Rows<3>, 1, 1>(l, p, s);
-    if (each <= 10) return launch_rows<16, Rows<5>, 1, 1>(l, p, s);
-    using Many = Wide<8, 2, 2, 2>;
-    if (each > 32 && wide_groups<Many>(l, p) >= 192 && wide_fits<Many>(l, p))
-        return launch_wide<Many>(l, p, s);
+    if (each <= 5) return launch_rows<Rows<3>, 1, 1>(l, p, s);
+    if (each <= 10) return launch_rows<Rows<5>, 1, 1>(l, p, s);
+    if (each > 32 && wide_groups<Wide256>(l, p) >= 192 && wide_fits<Wide256>(l, p))
+        return launch_many_rows(l, p, s);
     const int64_t groups = l.strips * ((each + 15) / 16 * experts);
-    if (groups >= 1024) return launch_rows<8, Rows<8>, 4, 1>(l, p, s);
-    if (groups >= 512) return launch_rows<8, Rows<8>, 2, 1>(l, p, s);
-    return launch_rows<8, Rows<8>, 1, 1>(l, p, s);
+    if (groups >= 1024 && l.parts < 4) return launch_rows<Rows<8>, 4, 1>(l, p, s);
+    if (groups >= 512) return launch_rows<Rows<8>, 2, 1>(l, p, s);
+    return launch_rows<Rows<8>, 1, 1>(l, p, s);
 }
 
 }  // namespace sgemm

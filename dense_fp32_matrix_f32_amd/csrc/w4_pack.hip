@@ -27,14 +27,14 @@ __global__ __launch_bounds__(256) void pack_kernel(W4Layout l, int64_t records,
         unsigned word[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            const int64_t k = (int64_t)b * kW4Block + 32 * j + 8 * q;
             word[j] = 0;
 #pragma unroll
             for (int i = 0; i < 8; i += 2) {
+                const int64_t k = (int64_t)b * kW4Block + 32 * j + w4_k(q, i);
                 unsigned byte = 0x88;
-                if (n < l.N && k + i < l.K) {
-                    byte = codes[(e * pairs + (k + i) / 2) * l.N + n];
-                    if (k + i + 1 >= l.K) byte = (byte & 15) | 0x80;
+                if (n < l.N && k < l.K) {
+                    byte = codes[(e * pairs + k / 2) * l.N + n];
+                    if (k + 1 >= l.K) byte = (byte & 15) | 0x80;
                 }
                 word[j] |= (byte & 15) << w4_shift(i);
                 word[j] |= (byte >> 4) << w4_shift(i + 1);
@@ -97,16 +97,18 @@ __global__ __launch_bounds__(256) void quantize_kernel(W4Layout l, int64_t items
                 rec[kW4Codes + l.parts * kW4Cols * l.scale_size + at] = (unsigned char)z;
             }
             const int len = min(l.group, kW4Block);
-            for (int w = 0; w < len; w += 8) {
-                const int kb = part * len + w;  // k within the block
+            for (int w = 0; w < len / 8; ++w) {
+                const int from = w / 4 * 32;  // this word's 32 k, from the part's first on
                 unsigned word = 0;
                 for (int i = 0; i < 8; ++i) {
+                    const int64_t ki = k + from + w4_k(w % 4, i);
                     int q = z;
-                    if (k + w + i < kend && s > 0.0f)
-                        q = (int)fminf(fmaxf(rintf(col[(k + w + i) * ldb] / s) + z, 0.0f), 15.0f);
+                    if (ki < kend && s > 0.0f)
+                        q = (int)fminf(fmaxf(rintf(col[ki * ldb] / s) + z, 0.0f), 15.0f);
                     word |= (unsigned)q << w4_shift(i);
                 }
-                *(unsigned *)(rec + 16 * (n % kW4Cols + 16 * (kb % 32 / 8)) + 4 * (kb / 32)) = word;
+                *(unsigned *)(rec + 16 * (n % kW4Cols + 16 * (w % 4)) +
+                              4 * ((part * len + from) / 32)) = word;
             }
         }
     }
@@ -127,11 +129,11 @@ __global__ __launch_bounds__(256) void unpack_kernel(W4Layout l, int64_t items,
                                    (int64_t)(k / kW4Block) * l.record;
         const int kb = k % kW4Block, c = n % kW4Cols;
         const unsigned word =
-            *(const unsigned *)(rec + 16 * (c + 16 * (kb % 32 / 8)) + 4 * (kb / 32));
+            *(const unsigned *)(rec + 16 * (c + 16 * w4_part(kb % 32)) + 4 * (kb / 32));
         const int at = c * l.parts + kb / (kW4Block / l.parts);
         const float s = w4_scale(rec + kW4Codes + at * l.scale_size, l.scale_type);
         const int z = l.zeros ? rec[kW4Codes + l.parts * kW4Cols * l.scale_size + at] : 8;
-        const int q = (word >> w4_shift(kb % 8)) & 15;
+        const int q = (word >> w4_shift(w4_index(kb % 32))) & 15;
         B[e * strideb + k * ldb + n] = s * (float)(q - z);
     }
 }

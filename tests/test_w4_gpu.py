@@ -112,9 +112,11 @@ def test_product_of_ordinary_sizes(rows, N, K):
 
 
 @pytest.mark.parametrize("rows,N,K,group", [(1000, 1500, 300, 32), (801, 2047, 129, 64),
-                                            (513, 2900, 1030, 128), (6200, 256, 4, 32)])
+                                            (513, 2900, 1030, 128), (6200, 256, 4, 32),
+                                            (2100, 2000, 200, 64), (2081, 1999, 385, 256)])
 def test_product_of_many_rows(rows, N, K, group):
-    """Sizes at which the kernel for many rows runs (192 work-groups of 32 x 256)."""
+    """Sizes at which the kernel for many rows runs (192 work-groups of 32 x 256, in its
+    wider form 256 of 32 x 512)."""
     torch = torch_cuda()
     rng = np.random.default_rng(rows)
     for zeros, scale_type, exact in [(True, "float32", True), (False, "bfloat16", False),
