@@ -16,11 +16,11 @@ namespace {
 template <class C>
 __global__ __launch_bounds__(C::THREADS, C::OCC) void grouped_kernel(GroupedProblem p, int tiles_n) {
     __shared__ __attribute__((aligned(16))) float lds[C::LDS_FLOATS];
-    const int tiles_m = count_blocks(p.offsets, p.experts, p.rows, C::BM);
     // (offsets that are no running sum can give more blocks than were launched, or a
-    // count past the int range, here negative)
-    const int64_t tiles = (int64_t)tiles_m * tiles_n;
-    if ((int64_t)blockIdx.x >= tiles) return;
+    // count that wrapped to a negative one)
+    const int tiles_m = min(count_blocks(p.offsets, p.experts, p.rows, C::BM),
+                            (int)(gridDim.x / (unsigned)tiles_n));
+    if ((int)blockIdx.x >= tiles_m * tiles_n) return;
     int tm, tn;
     tile_order(blockIdx.x, tiles_m, tiles_n, C::GROUP_M, &tm, &tn);
     int e, first, end;

@@ -44,17 +44,21 @@ __device__ __forceinline__ int bucket_of(const SortArgs &a, int f) {
     return e < 0 || e >= a.experts ? a.experts : e;
 }
 
-// counts of this wave's run into its row of `mine` (cleared before)
-__device__ __forceinline__ void count_run(const SortArgs &a, int begin, int *mine) {
-    const int n = a.p.count(), lane = threadIdx.x & 63;
-    for (int f = begin + lane; f < min(n, begin + a.run); f += 64)
-        atomicAdd(&mine[bucket_of(a, f)], 1);  // sums of ones: any order gives the same
-}
+// The pairs of this wave (none, where its run starts past the last pair).
+struct Run {
+    int64_t begin, end;
 
-__device__ __forceinline__ int run_begin(const SortArgs &a) {
-    // clamped: a chunk that starts past the last pair is empty
-    const int64_t b = ((int64_t)blockIdx.x * kSortWaves + (threadIdx.x >> 6)) * a.run;
-    return (int)min(b, (int64_t)a.p.count());
+    __device__ __forceinline__ explicit Run(const SortArgs &a) {
+        const int64_t n = a.p.count();
+        begin = min(((int64_t)blockIdx.x * kSortWaves + (threadIdx.x >> 6)) * a.run, n);
+        end = min(begin + a.run, n);
+    }
+};
+
+// The run's pairs by bucket, added to `mine`.
+__device__ __forceinline__ void count_run(const SortArgs &a, const Run &run, int *mine) {
+    for (int64_t f = run.begin + (threadIdx.x & 63); f < run.end; f += 64)
+        atomicAdd(&mine[bucket_of(a, (int)f)], 1);  // sums of ones: any order gives the same
 }
 
 __global__ __launch_bounds__(kSortThreads) void sort_count_kernel(SortArgs a) {
@@ -62,7 +66,7 @@ __global__ __launch_bounds__(kSortThreads) void sort_count_kernel(SortArgs a) {
     const int buckets = a.experts + 1;
     for (int e = threadIdx.x; e < buckets; e += kSortThreads) hist[e] = 0;
     __syncthreads();
-    count_run(a, run_begin(a), hist);
+    count_run(a, Run(a), hist);
     __syncthreads();
     for (int e = threadIdx.x; e < buckets; e += kSortThreads)
         a.counts[(int64_t)blockIdx.x * buckets + e] = hist[e];
@@ -72,13 +76,13 @@ __global__ __launch_bounds__(kSortThreads) void sort_place_kernel(SortArgs a, in
                                                                   int *order, int *position) {
     extern __shared__ int next[];  // [wave][bucket]: the place of the next pair
     __shared__ int sums[kSortWaves];
-    const int buckets = a.experts + 1, n = a.p.count();
+    const int buckets = a.experts + 1;
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
     for (int i = tid; i < buckets * kSortWaves; i += kSortThreads) next[i] = 0;
     __syncthreads();
-    const int begin = run_begin(a);
+    const Run run(a);
     int *mine = next + wave * buckets;
-    count_run(a, begin, mine);
+    count_run(a, run, mine);
     __syncthreads();
 
     // one work-item for each bucket (kSortBuckets <= kSortThreads)
@@ -112,9 +116,9 @@ __global__ __launch_bounds__(kSortThreads) void sort_place_kernel(SortArgs a, in
     }
     __syncthreads();
 
-    for (int base = begin; base < min(n, begin + a.run); base += 64) {
-        const int f = base + lane;
-        const bool have = f < min(n, begin + a.run);
+    for (int64_t base = run.begin; base < run.end; base += 64) {
+        const int f = (int)(base + lane);  // used where it is a pair
+        const bool have = base + lane < run.end;
         const int e = have ? bucket_of(a, f) : buckets;
         // the lanes with the same bucket
         unsigned long long same = __ballot(have);
@@ -367,7 +371,10 @@ __global__ __launch_bounds__(1024) void combine_grad_kernel(
 // Columns of a work-group's piece: all of them, or with too few tokens to fill the
 // chip pieces of one vector a lane.
 int span_for(int64_t groups, int width, int lanes) {
-    return groups >= 1024 ? width : 4 * lanes;
+    if (groups >= 1024) return width;
+    // the grid's second axis ends at 65535
+    const int64_t least = ((int64_t)width + 65534) / 65535, vector = 4ll * lanes;
+    return (int)((least + vector - 1) / vector * vector);
 }
 
 }  // namespace

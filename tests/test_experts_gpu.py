@@ -373,6 +373,55 @@ def test_grouped_follows_no_offset_out_of_its_rows():
         sg.grouped_matmul_ta(A, A, off)
 
 
+def test_offsets_that_name_more_rows_than_there_are():
+    """Every other expert claims all rows: more blocks than the launch holds.  Nothing
+    outside the rows is touched, and rows that are written hold some expert's product."""
+    torch = torch_cuda()
+    rows, K, N, experts = 200, 40, 300, 150
+    off = torch.tensor([0, 2**31 - 1] * (experts // 2) + [0], dtype=torch.int32, device="cuda")
+    A, B = torch.ones((rows, K), device="cuda"), torch.ones((experts, K, N), device="cuda")
+    buf = torch.full((rows + 400, N), SENT, device="cuda")
+    sg.grouped_matmul(A, B, off, out=buf[200:400])
+    assert int((buf[:200] != SENT).sum()) == 0 and int((buf[400:] != SENT).sum()) == 0
+    inside = buf[200:400]
+    assert ((inside == SENT) | (inside == K)).all()
+    C = sg.grouped_matmul_ta(A, torch.ones((rows, 24), device="cuda"), off)
+    assert C[0::2].eq(rows).all() and C[1::2].eq(0).all()
+    w = sg.w4_quantize(torch.full((experts, 64, N), 7.0, device="cuda"), group=32)
+    buf.fill_(SENT)
+    sg.matmul_w4(torch.ones((rows, 64), device="cuda"), w, offsets=off, out=buf[200:400])
+    assert int((buf[:200] != SENT).sum()) == 0 and int((buf[400:] != SENT).sum()) == 0
+    inside = buf[200:400]
+    assert ((inside == SENT) | (inside == 448)).all()
+
+
+def test_combine_grad_of_one_side_only():
+    """drows or dweights may be left out, and rows with the latter."""
+    torch = torch_cuda()
+    for tokens, top, width in [(5, 3, 70), (600, 6, 1500), (3, 9, 5000)]:
+        r = routing_of(tokens, top, 7, seed=width)
+        n = tokens * top
+        y, dy = torch.randn((n, width), device="cuda"), torch.randn((tokens, width), device="cuda")
+        w = torch.rand((tokens, top), device="cuda")
+        drows, dw = torch.full((n, width), SENT, device="cuda"), None
+        _, dw = sg.combine_rows_grad(dy, y, r, w, drows=drows)
+        one = torch.full((n, width), SENT, device="cuda")
+        s = torch.cuda.current_stream().cuda_stream
+        args = (tokens, top, width, r.position.data_ptr(), w.data_ptr(), top)
+        assert sg.sgemm_f32_route_combine_grad(*args, 0, width, dy.data_ptr(), width,
+                                               one.data_ptr(), width, 0, s) == 0
+        assert torch.equal(one, drows)
+        two = torch.empty((tokens, top), device="cuda")
+        assert sg.sgemm_f32_route_combine_grad(*args, y.data_ptr(), width, dy.data_ptr(), width, 0,
+                                               width, two.data_ptr(), s) == 0
+        assert torch.equal(two, dw)
+        # no columns: the sums are empty
+        two.fill_(SENT)
+        assert sg.sgemm_f32_route_combine_grad(tokens, top, 0, r.position.data_ptr(), 0, top, 0, 1,
+                                               0, 1, 0, 1, two.data_ptr(), s) == 0
+        assert two.eq(0).all()
+
+
 def test_one_matrix_for_all_experts():
     torch = torch_cuda()
     rng = np.random.default_rng(5)
