@@ -33,12 +33,17 @@ class Routing(NamedTuple):
 
 
 def _pairs(routing):
-    """(tokens, top) of a routing, whose positions are checked."""
+    """(positions, tokens, top, GPU number) of a routing, whose positions are checked."""
     position = routing.position
-    if not isinstance(position, torch.Tensor) or position.dim() != 2:
+    if (not isinstance(position, torch.Tensor) or position.dtype is not torch.int32
+            or position.dim() != 2):
         raise TypeError("routing.position must be a 2-D int32 torch tensor")
-    dense(position, position.shape, "routing.position", torch.int32, None)
-    return position.shape
+    device = position.get_device()
+    if device < 0:
+        place(position, "routing.position", None)
+    if not position.is_contiguous():
+        raise ValueError("routing.position must be contiguous")
+    return position, *position.shape, device
 
 
 def _offsets(offsets, device):
@@ -78,17 +83,16 @@ def gather_rows(x, routing, out=None, stream=None):
     """Row p of the result is the row of x (tokens x width) whose token is at place p
     of the routing.  Rows past the last place are left as they are in ``out`` (and
     hold anything in a result allocated here)."""
-    tokens, top = _pairs(routing)
-    ldx = matrix(x, tokens, None, "x", device=routing.position.get_device())
+    position, tokens, top, device = _pairs(routing)
+    ldx = matrix(x, tokens, None, "x", device=device)
     width = x.shape[1]
-    made = []
     if out is None:
         out = x.new_empty((tokens * top, width))
-        made.append(out)
-    device = x.get_device()
-    ldo = matrix(out, tokens * top, width, "out", device=device)
+        made, ldo = (out,), width or 1
+    else:
+        made, ldo = (), matrix(out, tokens * top, width, "out", device=device)
     call("sgemm_f32_route_gather", device, stream, made, tokens, top, width,
-         routing.position.data_ptr(), x.data_ptr(), ldx, out.data_ptr(), ldo)
+         position.data_ptr(), x.data_ptr(), ldx, out.data_ptr(), ldo)
     return out
 
 
@@ -96,18 +100,17 @@ def combine_rows(rows, routing, weights=None, out=None, stream=None):
     """Each token's rows, times its weights (tokens x top; None: 1), added in the order of
     its choices: tokens x width.  Dropped pairs add nothing.  Without weights this is
     the gradient of gather_rows."""
-    tokens, top = _pairs(routing)
-    device = routing.position.get_device()
+    position, tokens, top, device = _pairs(routing)
     ldr = matrix(rows, tokens * top, None, "rows", device=device)
     width = rows.shape[1]
     ldw = 1 if weights is None else matrix(weights, tokens, top, "weights", device=device)
-    made = []
     if out is None:
         out = rows.new_empty((tokens, width))
-        made.append(out)
-    ldo = matrix(out, tokens, width, "out", device=device)
+        made, ldo = (out,), width or 1
+    else:
+        made, ldo = (), matrix(out, tokens, width, "out", device=device)
     call("sgemm_f32_route_combine", device, stream, made, tokens, top, width,
-         routing.position.data_ptr(), 0 if weights is None else weights.data_ptr(), ldw,
+         position.data_ptr(), 0 if weights is None else weights.data_ptr(), ldw,
          rows.data_ptr(), ldr, out.data_ptr(), ldo)
     return out
 
@@ -117,8 +120,7 @@ def combine_rows_grad(dout, rows, routing, weights=None, drows=None, stream=None
     gradient dout of its result.  dweights is None without weights.  Rows past the
     last place are left as they are in ``drows`` (and hold anything in a tensor
     allocated here)."""
-    tokens, top = _pairs(routing)
-    device = routing.position.get_device()
+    position, tokens, top, device = _pairs(routing)
     ldd = matrix(dout, tokens, None, "dout", device=device)
     width = dout.shape[1]
     ldr = matrix(rows, tokens * top, width, "rows", device=device)
@@ -134,9 +136,11 @@ def combine_rows_grad(dout, rows, routing, weights=None, drows=None, stream=None
     if drows is None:
         drows = rows.new_empty((tokens * top, width))
         made.append(drows)
-    lddr = matrix(drows, tokens * top, width, "drows", device=device)
+        lddr = width or 1
+    else:
+        lddr = matrix(drows, tokens * top, width, "drows", device=device)
     call("sgemm_f32_route_combine_grad", device, stream, made, tokens, top, width,
-         routing.position.data_ptr(), 0 if weights is None else weights.data_ptr(), ldw,
+         position.data_ptr(), 0 if weights is None else weights.data_ptr(), ldw,
          rows.data_ptr(), ldr, dout.data_ptr(), ldd, drows.data_ptr(), lddr,
          0 if dweights is None else dweights.data_ptr())
     return drows, dweights
@@ -180,13 +184,13 @@ def grouped_matmul(A, B, offsets, out=None, alpha=1.0, beta=0.0, stream=None):
         raise ValueError(f"inner dimensions differ: {K} vs {K2}")
     if _offsets(offsets, device) != experts:
         raise ValueError(f"{offsets.numel()} offsets for {experts} experts")
-    made = []
     if out is None:
         if beta != 0.0:
             raise ValueError("beta != 0 needs out")
         out = A.new_empty((rows, N))
-        made.append(out)
-    ldc = matrix(out, rows, N, "out", device=device)
+        made, ldc = (out,), N or 1
+    else:
+        made, ldc = (), matrix(out, rows, N, "out", device=device)
     call("sgemm_f32_grouped", device, stream, made, int(trans), rows, N, K, experts,
          offsets.data_ptr(), float(alpha), A.data_ptr(), lda, B.data_ptr(), ldb, strideb,
          float(beta), out.data_ptr(), ldc)
@@ -204,17 +208,18 @@ def grouped_matmul_ta(A, D, offsets, out=None, alpha=1.0, beta=0.0, stream=None)
     ldd = matrix(D, rows, None, "D", device=device)
     N = D.shape[1]
     experts = _offsets(offsets, device)
-    made = []
+    made = ()
     if out is None:
         if beta != 0.0:
             raise ValueError("beta != 0 needs out")
         out = A.new_empty((experts, M, N))
-        made.append(out)
-    elif tuple(out.shape) != (experts, M, N):
-        raise ValueError("out has the wrong shape")
-    ldc, stridec, trans = _stack(out, "out", device)
-    if trans:
-        raise ValueError("out must hold row-major matrices")
+        made, ldc, stridec = (out,), N or 1, M * N
+    else:
+        if tuple(out.shape) != (experts, M, N):
+            raise ValueError("out has the wrong shape")
+        ldc, stridec, trans = _stack(out, "out", device)
+        if trans:
+            raise ValueError("out must hold row-major matrices")
     call("sgemm_f32_grouped_ta", device, stream, made, rows, M, N, experts, offsets.data_ptr(),
          float(alpha), A.data_ptr(), lda, D.data_ptr(), ldd, float(beta), out.data_ptr(), ldc,
          stridec)

@@ -117,11 +117,11 @@ def matmul_w4(A, w, offsets=None, out=None, stream=None):
             raise ValueError(f"{w.experts} matrices need offsets")
     elif _offsets(offsets, device) != w.experts:
         raise ValueError(f"{offsets.numel()} offsets for {w.experts} experts")
-    made = []
     if out is None:
         out = A.new_empty((rows, w.N))
-        made.append(out)
-    ldc = matrix(out, rows, w.N, "out", device=device)
+        made, ldc = (out,), w.N or 1
+    else:
+        made, ldc = (), matrix(out, rows, w.N, "out", device=device)
     if offsets is None:
         call("sgemm_f32_w4", device, stream, made, rows, w.N, w.K, A.data_ptr(), lda,
              w.packed.data_ptr(), w.group, w.scale_type, int(w.zeros), out.data_ptr(), ldc)
