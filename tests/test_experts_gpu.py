@@ -422,6 +422,46 @@ def test_combine_grad_of_one_side_only():
         assert two.eq(0).all()
 
 
+def test_arrays_beyond_32_bits():
+    """Rows past the 2^31st element, and matrices past the 2^32nd byte."""
+    torch = torch_cuda()
+    tokens, top, width, experts = 270_000, 2, 4096, 3
+    ids = torch.randint(0, experts, (tokens, top), dtype=torch.int32, device="cuda")
+    r = sg.sort_by_expert(ids, experts)
+    x = torch.randint(-8, 9, (tokens, 1), device="cuda").float() + \
+        torch.arange(width, device="cuda") % 16
+    rows = sg.gather_rows(x, r)
+    assert rows.numel() > 2**31
+    for t in (0, tokens // 2, tokens - 1):
+        for j in range(top):
+            assert torch.equal(rows[int(r.position[t, j])], x[t])
+    assert torch.equal(rows[-1], x[int(r.order[-1]) // top])
+    back = sg.combine_rows(rows, r)
+    assert torch.equal(back, 2 * x)
+    del back
+    w = torch.full((tokens, top), 0.5, device="cuda")
+    drows, dw = sg.combine_rows_grad(x, rows, r, w)
+    assert torch.equal(drows[-1], 0.5 * x[int(r.order[-1]) // top])
+    assert torch.equal(dw[-1].double(), (x[-1].double() ** 2).sum().expand(2))
+    del rows, drows, x
+
+    experts, K, N, n = 18, 8192, 8192, 40
+    B = torch.zeros((experts, K, N), device="cuda")
+    last = torch.randint(-2, 3, (K, N), device="cuda").float()
+    B[-1] = last
+    A = torch.randint(-2, 3, (n, K), device="cuda").float()
+    off = torch.tensor([0] * experts + [n], dtype=torch.int32, device="cuda")
+    off[-2] = 3
+    for mat in (B, B.transpose(1, 2)):
+        C = sg.grouped_matmul(A, mat, off)
+        want = A.double() @ (last if mat is B else last.t()).double()
+        want[:3] = 0
+        assert torch.equal(C.double(), want)
+    dB = sg.grouped_matmul_ta(A, C, off)
+    assert torch.equal(dB[-1].double(), A[3:].double().t() @ C[3:].double())
+    assert dB[-2].eq(0).all() and dB[0].eq(0).all()
+
+
 def test_one_matrix_for_all_experts():
     torch = torch_cuda()
     rng = np.random.default_rng(5)

@@ -331,6 +331,62 @@ def test_quantized_product_next_to_the_full_one():
                                                         float(A.abs().sum(1).max()) + float(mag.max()) * 504)
 
 
+def test_packed_weights_beyond_32_bits():
+    torch = torch_cuda()
+    experts, K, N = 66, 8192, 16384
+    codes = torch.full((experts, K // 2, N), 0x88, dtype=torch.uint8, device="cuda")
+    codes[-1] = torch.randint(0, 256, (K // 2, N), dtype=torch.uint8, device="cuda")
+    scales = torch.ones((experts, K // 128, N), dtype=torch.float16, device="cuda")
+    w = sg.w4_pack(codes, scales, K=K, group=128)
+    assert w.packed.numel() > 2**32
+    one = sg.w4_pack(codes[-1].contiguous(), scales[-1].contiguous(), K=K, group=128)
+    W = torch.stack((codes[-1] & 15, codes[-1] >> 4), 1).flatten(0, 1).double() - 8
+    del codes
+    for rows in (1, 4, 20, 70):
+        x = torch.randint(-2, 3, (rows, K), device="cuda").float()
+        off = torch.tensor([0] * experts + [rows], dtype=torch.int32, device="cuda")
+        got = sg.matmul_w4(x, w, offsets=off)
+        assert torch.equal(got.double(), x.double() @ W)
+        assert torch.equal(got, sg.matmul_w4(x, one))
+    out = torch.empty((1, K, N), device="cuda")
+    assert sg.sgemm_f32_w4_unpack(1, N, K, 128, w.scale_type, 0,
+                                  w.packed.data_ptr() + (experts - 1) * (w.packed.numel() // experts),
+                                  w.packed.numel() // experts, out.data_ptr(), N, K * N,
+                                  torch.cuda.current_stream().cuda_stream) == 0
+    assert torch.equal(out[0].double(), W)
+
+
+def test_calls_from_several_threads_and_streams():
+    """Products with the same weights from four host threads, each on its own stream."""
+    import threading
+    torch = torch_cuda()
+    rng = np.random.default_rng(21)
+    codes, s, z, W, _ = make(rng, 1, 700, 300, 32, True, True, "float16")
+    w = sg.w4_pack(codes[0], s[0], z[0], K=700, group=32)
+    xs = [rng.integers(-4, 5, (rows, 700)).astype(np.float32) for rows in (1, 5, 17, 90)]
+    dev = [torch.from_numpy(x).cuda() for x in xs]
+    torch.cuda.synchronize()
+    got = [[] for _ in xs]
+
+    def work(i):
+        stream = torch.cuda.Stream()
+        with torch.cuda.stream(stream):
+            for _ in range(20):
+                got[i].append(sg.matmul_w4(dev[i], w))
+        stream.synchronize()
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(len(xs))]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    for x, results in zip(xs, got):
+        assert len(results) == 20
+        want = x.astype(np.float64) @ W[0]
+        for c in results:
+            assert np.array_equal(c.double().cpu().numpy(), want)
+
+
 def test_graph_and_streams():
     torch = torch_cuda()
     rng = np.random.default_rng(9)
