@@ -415,7 +415,7 @@ hipError_t launch_rows(const W4Layout &l, const W4Problem &p, hipStream_t s) {
 // ---------------------------------------------------------------------------
 // Many rows.  Cutting A into parts costs about six vector operations a value, and
 // in the kernel above every work-group cuts its rows for 16 to 64 columns only.
-// Here a work-group computes BM rows by 256 or 512 columns over all k, its waves side by
+// Here a work-group computes 16 or 32 rows by 256 or 512 columns over all k, its waves side by
 // side in columns, and A is cut once for all of them, into two stages of LDS: while
 // one block of 128 k is multiplied, the next one's x is cut, one barrier a block.
 // The sums of A over 32 k (for the zero points) are formed on the way, in fp32.
@@ -659,21 +659,38 @@ hipError_t launch_wide(const W4Layout &l, const W4Problem &p, hipStream_t s) {
                   (int)wide_blocks<T>(p));
 }
 
-// 32 rows by 256 or 512 columns.  The wider block halves the cutting of A and the
-// reads of its parts from LDS; it is taken where it still gives every CU a
-// work-group, and not with four scales of a column in a block, which need more
-// registers than it leaves (512 rows 8192 x 4096, group 128: 90.4 against 94.4 us;
-// 2048 rows 4096 x 4096, group 64: 191 against 225; 512 rows 4096 x 4096, group 32:
-// 252 against 67).
+// 16 rows by 256 columns, or 32 by 512 (32 by 256 with four scales of a column in a
+// block, which need more registers than the larger leaves).  A larger block cuts A for
+// more columns and unpacks codes for more rows; it is taken where it still gives every
+// CU a work-group (two of the middle one).  Times in us:
+//                                          16 x 256  32 x 256  32 x 512
+//   256 rows 4096 x 4096, group 128          33        51
+//   1000 rows by expert, 16 x 2048 x 2048    47        58
+//   512 rows 4096 x 4096, group 32           66        65       252
+//   512 rows 8192 x 4096, group 128         100        94        88
+//   2048 rows 4096 x 4096, group 64         220       225       191
+using Wide16 = Wide<8, 1, 2, 2>;
 using Wide256 = Wide<8, 2, 2, 2>;
 using Wide512 = Wide<8, 2, 4, 2>;
 
+template <int PARTS>
+hipError_t launch_wide_as(const W4Layout &l, const W4Problem &p, hipStream_t s) {
+    using Large = typename std::conditional<PARTS == 4, Wide256, Wide512>::type;
+    const int least = (PARTS == 4 ? 2 : 1) * compute_units();
+    return wide_groups<Large>(l, p) >= least ? launch_wide<Large, PARTS>(l, p, s)
+                                             : launch_wide<Wide16, PARTS>(l, p, s);
+}
+
+// Whether there are rows enough for these kernels, and their offsets fit.
+bool many_rows(const W4Layout &l, const W4Problem &p) {
+    return wide_groups<Wide16>(l, p) >= compute_units() && wide_fits<Wide512>(l, p);
+}
+
 hipError_t launch_many_rows(const W4Layout &l, const W4Problem &p, hipStream_t s) {
-    const bool wider = wide_groups<Wide512>(l, p) >= compute_units();
     switch (l.parts) {
-    case 4: return launch_wide<Wide256, 4>(l, p, s);
-    case 2: return wider ? launch_wide<Wide512, 2>(l, p, s) : launch_wide<Wide256, 2>(l, p, s);
-    default: return wider ? launch_wide<Wide512, 1>(l, p, s) : launch_wide<Wide256, 1>(l, p, s);
+    case 4: return launch_wide_as<4>(l, p, s);
+    case 2: return launch_wide_as<2>(l, p, s);
+    default: return launch_wide_as<1>(l, p, s);
     }
 }
 
@@ -692,8 +709,9 @@ hipError_t launch_many_rows(const W4Layout &l, const W4Problem &p, hipStream_t s
 //   16    8192 x 8192, 64   two strips 19.1  one 32.8, four 24.6
 //   32    4096 x 4096, 128  two strips 10.6  one 17.2, four 13.5
 //   256 by expert, 16 x 1408 x 4096, 32: two strips 38.8, one 58, four 44
-//   64    4096 x 4096, 128  four strips 14.1 two 18.9; many-rows form 50
-//   128   4096 x 4096, 64   four strips 27.0 two 35.2; many-rows form 54
+//   64    4096 x 4096, 128  four strips 14.1 two 18.9; many rows 32
+//   128   4096 x 4096, 64   four strips 27.0 two 35.2; many rows 36
+//   256   4096 x 4096, 128  many rows 33     four strips 49
 //   512   4096 x 4096, 32   many rows 65     four strips 121
 //   512   8192 x 4096, 128  many rows 88     four strips 197
 // (4.5 us is 1.9 TB/s; a kernel that does nothing takes about 2.5.)  Slices of k over
@@ -714,8 +732,7 @@ hipError_t launch_w4(const W4Layout &l, const W4Problem &p, hipStream_t s) {
     }
     if (each <= 5) return launch_rows<Rows<3>, 1, 1>(l, p, s);
     if (each <= 10) return launch_rows<Rows<5>, 1, 1>(l, p, s);
-    if (each > 32 && wide_groups<Wide256>(l, p) >= 192 && wide_fits<Wide256>(l, p))
-        return launch_many_rows(l, p, s);
+    if (many_rows(l, p)) return launch_many_rows(l, p, s);
     const int64_t groups = l.strips * ((each + 15) / 16 * experts);
     if (groups >= 1024 && l.parts < 4) return launch_rows<Rows<8>, 4, 1>(l, p, s);
     if (groups >= 512) return launch_rows<Rows<8>, 2, 1>(l, p, s);

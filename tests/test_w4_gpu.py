@@ -111,12 +111,13 @@ def test_product_of_ordinary_sizes(rows, N, K):
         close(run(x, w), x.astype(np.float64) @ W[0], K, np.abs(x.astype(np.float64)) @ mag[0], "w4")
 
 
-@pytest.mark.parametrize("rows,N,K,group", [(1000, 1500, 300, 32), (801, 2047, 129, 64),
-                                            (513, 2900, 1030, 128), (6200, 256, 4, 32),
-                                            (2100, 2000, 200, 64), (2081, 1999, 385, 256)])
+@pytest.mark.parametrize("rows,N,K,group", [
+    (1000, 1500, 300, 32), (1001, 1500, 300, 256), (801, 2047, 129, 64),   # 16 x 256
+    (4100, 1000, 300, 32), (4111, 1023, 140, 32),                          # 32 x 256
+    (2100, 2000, 200, 64), (2081, 1999, 385, 256),                         # 32 x 512
+    (513, 2900, 1030, 128), (6200, 256, 4, 32)])
 def test_product_of_many_rows(rows, N, K, group):
-    """Sizes at which the kernel for many rows runs (192 work-groups of 32 x 256, in its
-    wider form 256 of 32 x 512)."""
+    """Sizes at which the kernels for many rows run, from one work-group a CU on."""
     torch = torch_cuda()
     rng = np.random.default_rng(rows)
     for zeros, scale_type, exact in [(True, "float32", True), (False, "bfloat16", False),
@@ -136,7 +137,7 @@ def test_product_of_many_rows(rows, N, K, group):
 @pytest.mark.parametrize("which", ["one has all", "ragged", "rows of no expert"])
 def test_product_of_many_rows_by_expert(which):
     torch = torch_cuda()
-    rows, N, K, experts = 900, 1300, 200, 16
+    rows, N, K, experts = 1000, 1300, 200, 16
     rng = np.random.default_rng(5)
     offsets = [int(o) for o in OFFSETS[which](rows, experts)]
     codes, s, z, W, mag = make(rng, experts, K, N, 64, True, True, "float16")
