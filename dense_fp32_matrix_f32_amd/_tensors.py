@@ -10,6 +10,7 @@ from torch._C import _cuda_getDevice as current_device
 from ._binding import SgemmError, lib
 
 INT_MAX = 2**31 - 1
+MOST = 2**31 - 65537   # the largest size that the operators take
 
 
 def matrix(t, rows, cols, name, dtype=torch.float32, device=None):

@@ -8,6 +8,7 @@
 #include "extent.h"
 
 using sgemm::Extent;
+using sgemm::valid_size;
 
 namespace {
 
@@ -32,15 +33,14 @@ Extent list(const void *p, int64_t n) { return sgemm::extent(p, 1, n, n, 4); }
 
 constexpr Extent kNone{0, 0};  // meets nothing
 
-// tokens, top and experts are sizes whose pairs fit an int.
 bool valid_pairs(int tokens, int top) {
-    return tokens >= 0 && top >= 0 && (int64_t)tokens * top <= INT32_MAX;
+    return valid_size(tokens) && valid_size(top) && (int64_t)tokens * top <= sgemm::kMaxSize;
 }
 
 }  // namespace
 
 extern "C" size_t sgemm_f32_route_workspace_size(int tokens, int top, int experts) {
-    if (!valid_pairs(tokens, top) || experts < 0 || experts == INT32_MAX) return 0;
+    if (!valid_pairs(tokens, top) || !valid_size(experts)) return 0;
     return sgemm::route_workspace({tokens, top}, experts);
 }
 
@@ -48,8 +48,8 @@ extern "C" hipError_t sgemm_f32_route_sort(int tokens, int top, int experts, con
                                            int ldids, int *offsets, int *order, int *position,
                                            void *workspace, size_t workspace_bytes,
                                            hipStream_t stream) {
-    if (!valid_pairs(tokens, top) || experts < 0 || experts == INT32_MAX ||
-        ldids < at_least_one(top) || offsets == nullptr)
+    if (!valid_pairs(tokens, top) || !valid_size(experts) || ldids < at_least_one(top) ||
+        offsets == nullptr)
         return hipErrorInvalidValue;
     const int n = tokens * top;
     const Extent o = list(offsets, (int64_t)experts + 1);
@@ -68,10 +68,10 @@ extern "C" hipError_t sgemm_f32_route_sort(int tokens, int top, int experts, con
                                     workspace, stream);
 }
 
-extern "C" hipError_t sgemm_f32_route_gather(int tokens, int top, int width,
-                                             const int *position, const float *x, int ldx, float *rows, int ldrows,
+extern "C" hipError_t sgemm_f32_route_gather(int tokens, int top, int width, const int *position,
+                                             const float *x, int ldx, float *rows, int ldrows,
                                              hipStream_t stream) {
-    if (!valid_pairs(tokens, top) || width < 0 || ldx < at_least_one(width) ||
+    if (!valid_pairs(tokens, top) || !valid_size(width) || ldx < at_least_one(width) ||
         ldrows < at_least_one(width))
         return hipErrorInvalidValue;
     const int n = tokens * top;
@@ -88,7 +88,7 @@ extern "C" hipError_t sgemm_f32_route_combine(int tokens, int top, int width, co
                                               const float *weights, int ldw, const float *rows,
                                               int ldrows, float *out, int ldout,
                                               hipStream_t stream) {
-    if (!valid_pairs(tokens, top) || width < 0 || ldrows < at_least_one(width) ||
+    if (!valid_pairs(tokens, top) || !valid_size(width) || ldrows < at_least_one(width) ||
         ldout < at_least_one(width) || (weights != nullptr && ldw < at_least_one(top)))
         return hipErrorInvalidValue;
     const int n = tokens * top;
@@ -110,7 +110,7 @@ extern "C" hipError_t sgemm_f32_route_combine_grad(int tokens, int top, int widt
                                                    const float *dout, int lddout, float *drows,
                                                    int lddrows, float *dweights,
                                                    hipStream_t stream) {
-    if (!valid_pairs(tokens, top) || width < 0 || lddout < at_least_one(width) ||
+    if (!valid_pairs(tokens, top) || !valid_size(width) || lddout < at_least_one(width) ||
         (dweights != nullptr && ldrows < at_least_one(width)) ||
         (drows != nullptr && lddrows < at_least_one(width)) ||
         ((weights != nullptr || dweights != nullptr) && ldw < at_least_one(top)))
@@ -138,9 +138,9 @@ extern "C" hipError_t sgemm_f32_grouped(int transb, int rows, int N, int K, int 
                                         const float *B, int ldb, long long strideb, float beta,
                                         float *C, int ldc, hipStream_t stream) {
     const bool tb = transb == SGEMM_F32_OP_T;
-    if ((!tb && transb != SGEMM_F32_OP_N) || rows < 0 || N < 0 || K < 0 || experts < 0 ||
-        strideb < 0 || lda < at_least_one(K) || ldb < at_least_one(tb ? K : N) ||
-        ldc < at_least_one(N))
+    if ((!tb && transb != SGEMM_F32_OP_N) || !valid_size(rows) || !valid_size(N) ||
+        !valid_size(K) || !valid_size(experts) || strideb < 0 || lda < at_least_one(K) ||
+        ldb < at_least_one(tb ? K : N) || ldc < at_least_one(N))
         return hipErrorInvalidValue;
     if (rows == 0 || N == 0 || experts == 0) return hipSuccess;
     if (offsets == nullptr || C == nullptr) return hipErrorInvalidValue;
@@ -161,8 +161,8 @@ extern "C" hipError_t sgemm_f32_grouped_ta(int rows, int M, int N, int experts,
                                            const int *offsets, float alpha, const float *A,
                                            int lda, const float *D, int ldd, float beta, float *C,
                                            int ldc, long long stridec, hipStream_t stream) {
-    if (rows < 0 || M < 0 || N < 0 || experts < 0 || lda < at_least_one(M) ||
-        ldd < at_least_one(N) || ldc < at_least_one(N))
+    if (!valid_size(rows) || !valid_size(M) || !valid_size(N) || !valid_size(experts) ||
+        lda < at_least_one(M) || ldd < at_least_one(N) || ldc < at_least_one(N))
         return hipErrorInvalidValue;
     if (M == 0 || N == 0 || experts == 0) return hipSuccess;
     // one C_e must not reach into the next

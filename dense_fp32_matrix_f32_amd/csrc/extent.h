@@ -1,5 +1,5 @@
-// extent.h -- byte ranges of the arrays of a call, for the overlap checks of the
-// entry points (host only, no HIP call).
+// extent.h -- sizes of a call, and byte ranges of its arrays for the overlap checks of
+// the entry points (host only, no HIP call).
 #pragma once
 
 #include <stddef.h>
@@ -34,6 +34,12 @@ inline Extent extent(const void *p, int64_t count, int64_t stride, int64_t rows,
                           (uint64_t)cols) *
                              size);
 }
+
+// The operators by expert and with 4-bit weights take sizes that stay inside 31 bits
+// when they are rounded up to blocks or stepped past by a grid.
+constexpr int kMaxSize = INT32_MAX - 65536;
+
+inline bool valid_size(int n) { return n >= 0 && n <= kMaxSize; }
 
 inline bool overlaps(Extent a, Extent b) { return a.lo < b.hi && b.lo < a.hi; }
 

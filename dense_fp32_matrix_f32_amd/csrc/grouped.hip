@@ -14,7 +14,8 @@ namespace {
 // once.  The ones there are get the XCD-aware order of the plain product, over all
 // experts' row blocks: those of one expert follow each other and share its matrix.
 template <class C>
-__global__ __launch_bounds__(C::THREADS, C::OCC) void grouped_kernel(GroupedProblem p, int tiles_n) {
+__global__ __launch_bounds__(C::THREADS, C::OCC) void grouped_kernel(GroupedProblem p,
+                                                                    int tiles_n) {
     __shared__ __attribute__((aligned(16))) float lds[C::LDS_FLOATS];
     // (offsets that are no running sum can give more blocks than were launched, or a
     // count that wrapped to a negative one)
@@ -90,7 +91,7 @@ template <class C>
 hipError_t launch_blocks(const GroupedProblem &p, hipStream_t s) {
     const int64_t tiles_n = ((int64_t)p.N + C::BN - 1) / C::BN;
     const int64_t blocks = most_blocks(p.rows, p.experts, C::BM) * tiles_n;
-    if (blocks > INT32_MAX) return hipErrorInvalidValue;
+    if (blocks > most_groups(C::THREADS)) return hipErrorInvalidValue;
     return launch(grouped_kernel<C>, dim3((unsigned)blocks), dim3(C::THREADS), 0, s, p,
                   (int)tiles_n);
 }
@@ -110,7 +111,7 @@ hipError_t launch_ta_blocks(const GroupedTaProblem &p, hipStream_t s) {
     const int64_t tiles_m = ((int64_t)p.M + C::BM - 1) / C::BM;
     const int64_t tiles_n = ((int64_t)p.N + C::BN - 1) / C::BN;
     const __int128 blocks = (__int128)tiles_m * tiles_n * p.experts;
-    if (blocks > INT32_MAX) return hipErrorInvalidValue;
+    if (blocks > most_groups(C::THREADS)) return hipErrorInvalidValue;
     return launch(grouped_ta_kernel<C>, dim3((unsigned)blocks), dim3(C::THREADS), 0, s, p,
                   (int)tiles_m, (int)tiles_n);
 }

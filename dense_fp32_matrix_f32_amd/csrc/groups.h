@@ -74,6 +74,10 @@ __device__ __forceinline__ int count_blocks(const int *__restrict__ offsets, int
     return count;
 }
 
+// The most work-groups of `threads` work-items that one launch holds: its work-items
+// are counted in 32 bits.
+constexpr int64_t most_groups(int threads) { return UINT32_MAX / threads; }
+
 // The most blocks find_block() can find: each expert with rows ends at most one
 // block short of full.
 inline int64_t most_blocks(int rows, int experts, int block) {

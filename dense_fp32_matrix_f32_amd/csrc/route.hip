@@ -143,40 +143,42 @@ __global__ __launch_bounds__(kSortThreads) void sort_place_kernel(SortArgs a, in
     }
 }
 
-// More experts than fit LDS: one work-group for each bucket.  It counts the pairs of
-// the buckets below its own, then walks all pairs in order and gives its own the
-// places from there on, ranked by a ballot in a wave and a running sum over waves.
+// More experts than fit LDS: one work-group for a bucket.  It counts the pairs of the
+// buckets below its own, then walks all pairs in order and gives its own the places
+// from there on, ranked by a ballot in a wave and a running sum over waves.
 __global__ __launch_bounds__(kSortThreads) void sort_each_kernel(SortArgs a, int *offsets,
                                                                  int *order, int *position) {
     __shared__ int sums[kSortWaves];
-    const int me = blockIdx.x, tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
     const int n = a.p.count();
-    int below = 0;
-    for (int64_t f = tid; f < n; f += kSortThreads) below += bucket_of(a, (int)f) < me;
-    for (int d = 32; d; d /= 2) below += __shfl_xor(below, d);
-    if (lane == 0) sums[wave] = below;
-    __syncthreads();
-    int place = 0;
-    for (int w = 0; w < kSortWaves; ++w) place += sums[w];
-    if (tid == 0) offsets[me] = place;
-    __syncthreads();
-    for (int64_t base = 0; base < n; base += kSortThreads) {
-        const int64_t f = base + tid;
-        const bool mine = f < n && bucket_of(a, (int)f) == me;
-        const unsigned long long who = __ballot(mine);
-        if (lane == 0) sums[wave] = __popcll(who);
+    for (int64_t me = blockIdx.x; me <= a.experts; me += gridDim.x) {
+        int below = 0;
+        for (int64_t f = tid; f < n; f += kSortThreads) below += bucket_of(a, (int)f) < me;
+        for (int d = 32; d; d /= 2) below += __shfl_xor(below, d);
+        if (lane == 0) sums[wave] = below;
         __syncthreads();
-        int at = place;
-        for (int w = 0; w < kSortWaves; ++w) {
-            if (w < wave) at += sums[w];
-            place += sums[w];
-        }
-        if (mine) {
-            at += __popcll(who & ((1ull << lane) - 1));
-            position[f] = me < a.experts ? at : -1;
-            order[at] = me < a.experts ? (int)f : -1;
-        }
+        int place = 0;
+        for (int w = 0; w < kSortWaves; ++w) place += sums[w];
+        if (tid == 0) offsets[me] = place;
         __syncthreads();
+        for (int64_t base = 0; base < n; base += kSortThreads) {
+            const int64_t f = base + tid;
+            const bool mine = f < n && bucket_of(a, (int)f) == me;
+            const unsigned long long who = __ballot(mine);
+            if (lane == 0) sums[wave] = __popcll(who);
+            __syncthreads();
+            int at = place;
+            for (int w = 0; w < kSortWaves; ++w) {
+                if (w < wave) at += sums[w];
+                place += sums[w];
+            }
+            if (mine) {
+                at += __popcll(who & ((1ull << lane) - 1));
+                position[f] = me < a.experts ? at : -1;
+                order[at] = me < a.experts ? (int)f : -1;
+            }
+            __syncthreads();
+        }
     }
 }
 
@@ -270,18 +272,18 @@ __global__ __launch_bounds__(256) void gather_kernel(Pairs p, int width, int lan
                                                      const float *__restrict__ x, int64_t ldx,
                                                      float *__restrict__ rows, int64_t ldrows) {
     const int per = 256 / lanes, lane = threadIdx.x % lanes;
-    const int64_t t = (int64_t)blockIdx.x * per + threadIdx.x / lanes;
-    if (t >= p.tokens) return;
     const int64_t begin = (int64_t)blockIdx.y * span, end = min((int64_t)width, begin + span);
-    for (int j0 = 0; j0 < p.top; j0 += J) {
-        const Choices k(p, t, j0, position, nullptr, 0);
-        for_columns(begin, end, lane, lanes, [&](int64_t c, auto vector) {
-            const auto v = load(x + t * ldx + c, vector);
+    for (int64_t t = (int64_t)blockIdx.x * per + threadIdx.x / lanes; t < p.tokens;
+         t += (int64_t)gridDim.x * per)
+        for (int j0 = 0; j0 < p.top; j0 += J) {
+            const Choices k(p, t, j0, position, nullptr, 0);
+            for_columns(begin, end, lane, lanes, [&](int64_t c, auto vector) {
+                const auto v = load(x + t * ldx + c, vector);
 #pragma unroll
-            for (int j = 0; j < J; ++j)
-                if (k.place[j] >= 0) store(rows + k.place[j] * ldrows + c, v);
-        });
-    }
+                for (int j = 0; j < J; ++j)
+                    if (k.place[j] >= 0) store(rows + k.place[j] * ldrows + c, v);
+            });
+        }
 }
 
 // out[t] = sum of weights[t, j] * rows[position[t, j]] in the order of j.
@@ -292,24 +294,25 @@ __global__ __launch_bounds__(256) void combine_kernel(Pairs p, int width, int la
                                                       int64_t ldrows, float *__restrict__ out,
                                                       int64_t ldout) {
     const int per = 256 / lanes, lane = threadIdx.x % lanes;
-    const int64_t t = (int64_t)blockIdx.x * per + threadIdx.x / lanes;
-    if (t >= p.tokens) return;
     const int64_t begin = (int64_t)blockIdx.y * span, end = min((int64_t)width, begin + span);
-    const Choices first(p, t, 0, position, weights, ldw);
-    for_columns(begin, end, lane, lanes, [&](int64_t c, auto vector) {
-        Cols<decltype(vector)::value> sum = {};
-        auto add = [&](const Choices &k) {
-            Cols<decltype(vector)::value> v[J];
+    for (int64_t t = (int64_t)blockIdx.x * per + threadIdx.x / lanes; t < p.tokens;
+         t += (int64_t)gridDim.x * per) {
+        const Choices first(p, t, 0, position, weights, ldw);
+        for_columns(begin, end, lane, lanes, [&](int64_t c, auto vector) {
+            Cols<decltype(vector)::value> sum = {};
+            auto add = [&](const Choices &k) {
+                Cols<decltype(vector)::value> v[J];
 #pragma unroll
-            for (int j = 0; j < J; ++j) v[j] = load(rows + k.row(j) * ldrows + c, vector);
+                for (int j = 0; j < J; ++j) v[j] = load(rows + k.row(j) * ldrows + c, vector);
 #pragma unroll
-            for (int j = 0; j < J; ++j)
-                if (k.place[j] >= 0) sum = mul_add(k.w[j], v[j], sum);
-        };
-        if (p.top > 0) add(first);
-        for (int j0 = J; j0 < p.top; j0 += J) add(Choices(p, t, j0, position, weights, ldw));
-        store(out + t * ldout + c, sum);
-    });
+                for (int j = 0; j < J; ++j)
+                    if (k.place[j] >= 0) sum = mul_add(k.w[j], v[j], sum);
+            };
+            if (p.top > 0) add(first);
+            for (int j0 = J; j0 < p.top; j0 += J) add(Choices(p, t, j0, position, weights, ldw));
+            store(out + t * ldout + c, sum);
+        });
+    }
 }
 
 // The gradients of a token, four choices at a time: its dout is read once for them;
@@ -322,56 +325,66 @@ __global__ __launch_bounds__(1024) void combine_grad_kernel(
     float *__restrict__ dweights) {
     __shared__ float part[16][J];
     const int per = blockDim.x / lanes, lane = threadIdx.x % lanes;
-    const int64_t token = (int64_t)blockIdx.x * per + threadIdx.x / lanes;
-    const bool have = token < p.tokens;  // every work-item reaches the barriers
-    const int64_t t = have ? token : 0;
-    for (int j0 = 0; j0 < p.top; j0 += J) {
-        const Choices k(p, t, j0, position, weights, ldw);
-        float dot[J] = {};
-        if (have) {
-            for_columns(0, width, lane, lanes, [&](int64_t c, auto vector) {
-                typedef Cols<decltype(vector)::value> V;
-                const V g = load(dout + t * lddout + c, vector);
-                if (dweights != nullptr) {
-                    V y[J];
+    for (int64_t t0 = (int64_t)blockIdx.x * per; t0 < p.tokens; t0 += (int64_t)gridDim.x * per) {
+        const int64_t token = t0 + threadIdx.x / lanes;
+        const bool have = token < p.tokens;  // every work-item reaches the barriers
+        const int64_t t = have ? token : 0;
+        for (int j0 = 0; j0 < p.top; j0 += J) {
+            const Choices k(p, t, j0, position, weights, ldw);
+            float dot[J] = {};
+            if (have) {
+                for_columns(0, width, lane, lanes, [&](int64_t c, auto vector) {
+                    typedef Cols<decltype(vector)::value> V;
+                    const V g = load(dout + t * lddout + c, vector);
+                    if (dweights != nullptr) {
+                        V y[J];
 #pragma unroll
-                    for (int j = 0; j < J; ++j) y[j] = load(rows + k.row(j) * ldrows + c, vector);
+                        for (int j = 0; j < J; ++j)
+                            y[j] = load(rows + k.row(j) * ldrows + c, vector);
 #pragma unroll
-                    for (int j = 0; j < J; ++j)
-                        if (k.place[j] >= 0) dot[j] = dot_add(g, y[j], dot[j]);
-                }
-                if (drows != nullptr) {
+                        for (int j = 0; j < J; ++j)
+                            if (k.place[j] >= 0) dot[j] = dot_add(g, y[j], dot[j]);
+                    }
+                    if (drows != nullptr) {
 #pragma unroll
-                    for (int j = 0; j < J; ++j)
-                        if (k.place[j] >= 0) store(drows + k.place[j] * lddrows + c, k.w[j] * g);
-                }
-            });
-        }
-        if (dweights == nullptr) continue;
-#pragma unroll
-        for (int j = 0; j < J; ++j)
-            for (int d = min(lanes, 64) / 2; d > 0; d /= 2) dot[j] += __shfl_xor(dot[j], d);
-        if (lanes > 64) {
-            const int wave = threadIdx.x >> 6;
-            __syncthreads();  // the last four choices' sums have been read
-            if ((threadIdx.x & 63) == 0) {
-#pragma unroll
-                for (int j = 0; j < J; ++j) part[wave][j] = dot[j];
+                        for (int j = 0; j < J; ++j)
+                            if (k.place[j] >= 0)
+                                store(drows + k.place[j] * lddrows + c, k.w[j] * g);
+                    }
+                });
             }
-            __syncthreads();
-            if (lane == 0) {
-#pragma unroll
-                for (int j = 0; j < J; ++j)
-                    for (int i = 1; i < lanes / 64; ++i) dot[j] += part[wave + i][j];
-            }
-        }
-        if (have && lane == 0) {
+            if (dweights == nullptr) continue;
 #pragma unroll
             for (int j = 0; j < J; ++j)
-                if (j0 + j < p.top)
-                    dweights[t * ldw + j0 + j] = k.place[j] >= 0 ? dot[j] : 0.0f;
+                for (int d = min(lanes, 64) / 2; d > 0; d /= 2) dot[j] += __shfl_xor(dot[j], d);
+            if (lanes > 64) {
+                const int wave = threadIdx.x >> 6;
+                __syncthreads();  // the last four choices' sums have been read
+                if ((threadIdx.x & 63) == 0) {
+#pragma unroll
+                    for (int j = 0; j < J; ++j) part[wave][j] = dot[j];
+                }
+                __syncthreads();
+                if (lane == 0) {
+#pragma unroll
+                    for (int j = 0; j < J; ++j)
+                        for (int i = 1; i < lanes / 64; ++i) dot[j] += part[wave + i][j];
+                }
+            }
+            if (have && lane == 0) {
+#pragma unroll
+                for (int j = 0; j < J; ++j)
+                    if (j0 + j < p.top)
+                        dweights[t * ldw + j0 + j] = k.place[j] >= 0 ? dot[j] : 0.0f;
+            }
         }
     }
+}
+
+// Work-groups of a launch; further tokens and buckets are taken in turn (1024
+// work-items each stay below 2^32).
+unsigned route_groups(int64_t groups) {
+    return (unsigned)(groups < (1 << 21) ? groups : 1 << 21);
 }
 
 // Columns of a work-group's piece: all of them, or with too few tokens to fill the
@@ -396,8 +409,8 @@ hipError_t launch_route_sort(Pairs p, int experts, const int *ids, int64_t ldids
     SortArgs a{p, experts, ids, ldids, 0, 0, (int *)workspace};
     sort_cut(p.count(), &a.run, &a.chunks);
     if (experts >= kSortBuckets)
-        return launch(sort_each_kernel, dim3((unsigned)experts + 1), dim3(kSortThreads), 0, s, a,
-                      offsets, order, position);
+        return launch(sort_each_kernel, dim3(route_groups((int64_t)experts + 1)),
+                      dim3(kSortThreads), 0, s, a, offsets, order, position);
     if (a.chunks == 1) {
         a.counts = nullptr;
     } else {
@@ -415,7 +428,7 @@ hipError_t launch_route_gather(Pairs p, int width, const int *position, const fl
     const int lanes = lanes_for(width, 256);
     const int64_t groups = ((int64_t)p.tokens * lanes + 255) / 256;
     const int span = span_for(groups, width, lanes);
-    const dim3 grid((unsigned)groups, (unsigned)(((int64_t)width + span - 1) / span));
+    const dim3 grid(route_groups(groups), (unsigned)(((int64_t)width + span - 1) / span));
     return launch(gather_kernel, grid, dim3(256), 0, s, p, width, lanes, span, position, x, ldx,
                   rows, ldrows);
 }
@@ -426,7 +439,7 @@ hipError_t launch_route_combine(Pairs p, int width, const int *position, const f
     const int lanes = lanes_for(width, 256);
     const int64_t groups = ((int64_t)p.tokens * lanes + 255) / 256;
     const int span = span_for(groups, width, lanes);
-    const dim3 grid((unsigned)groups, (unsigned)(((int64_t)width + span - 1) / span));
+    const dim3 grid(route_groups(groups), (unsigned)(((int64_t)width + span - 1) / span));
     return launch(combine_kernel, grid, dim3(256), 0, s, p, width, lanes, span, position, weights,
                   ldw, rows, ldrows, out, ldout);
 }
@@ -440,7 +453,7 @@ hipError_t launch_route_combine_grad(Pairs p, int width, const int *position,
     const int lanes = lanes_for(width, p.tokens < 512 ? 1024 : 256);
     const int threads = lanes > 256 ? lanes : 256;
     const int64_t groups = ((int64_t)p.tokens * lanes + threads - 1) / threads;
-    return launch(combine_grad_kernel, dim3((unsigned)groups), dim3((unsigned)threads), 0, s, p,
+    return launch(combine_grad_kernel, dim3(route_groups(groups)), dim3((unsigned)threads), 0, s, p,
                   width, lanes, position, weights, ldw, rows, ldrows, dout, lddout, drows,
                   lddrows, dweights);
 }

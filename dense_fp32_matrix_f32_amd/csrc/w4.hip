@@ -11,8 +11,9 @@
 //     run), so the byte pairs of a word become bf16 pairs by the conversion
 //     instruction with scale 2^9: seven vector operations for eight codes;
 //   * A[i][k] is cut into three bf16 parts that add up to it exactly (each part the
-//     truncation of what is left, 8 bits at a time).  The parts of a row are rows of
-//     their own in the matrix instruction: five rows of A fill one instruction of 16;
+//     truncation of what is left, 8 bits at a time; only bits below 2^-133, bf16's
+//     smallest number, are lost).  The parts of a row are rows of their own in the
+//     matrix instruction: five rows of A fill one instruction of 16;
 //   * z enters as z times the sum of A[i][k] over the group, which one more matrix
 //     instruction with a matrix of ones forms in the registers' own layout.
 // Products of parts and codes are exact in fp32 and are added in fp32; each group's
@@ -403,7 +404,7 @@ hipError_t launch_rows(const W4Layout &l, const W4Problem &p, hipStream_t s) {
     const int64_t row_blocks = p.offsets != nullptr ? most_blocks(p.rows, p.experts, R::MR)
                                                     : ((int64_t)p.rows + R::MR - 1) / R::MR;
     const int64_t groups = ((int64_t)l.strips + CT - 1) / CT * row_blocks;
-    if (groups > INT32_MAX) return hipErrorInvalidValue;
+    if (groups > most_groups(W * 64)) return hipErrorInvalidValue;
     const dim3 grid((unsigned)groups), block(W * 64);
     switch (l.parts) {
     case 4: return launch(w4_kernel<R, CT, 4, D>, grid, block, 0, s, l, p, (int)row_blocks);
@@ -415,9 +416,9 @@ hipError_t launch_rows(const W4Layout &l, const W4Problem &p, hipStream_t s) {
 // ---------------------------------------------------------------------------
 // Many rows.  Cutting A into parts costs about six vector operations a value, and
 // in the kernel above every work-group cuts its rows for 16 to 64 columns only.
-// Here a work-group computes 16 or 32 rows by 256 or 512 columns over all k, its waves side by
-// side in columns, and A is cut once for all of them, into two stages of LDS: while
-// one block of 128 k is multiplied, the next one's x is cut, one barrier a block.
+// Here a work-group computes 16 or 32 rows by 256 or 512 columns over all k, its waves
+// side by side in columns, and A is cut once for all of them, into two stages of LDS:
+// while one block of 128 k is multiplied, the next one's x is cut, one barrier a block.
 // The sums of A over 32 k (for the zero points) are formed on the way, in fp32.
 template <int W_, int RTW_, int CTW_, int D_>
 struct Wide {
@@ -654,7 +655,7 @@ bool wide_fits(const W4Layout &l, const W4Problem &p) {
 template <class T, int PARTS>
 hipError_t launch_wide(const W4Layout &l, const W4Problem &p, hipStream_t s) {
     const int64_t groups = wide_groups<T>(l, p);
-    if (groups > INT32_MAX) return hipErrorInvalidValue;
+    if (groups > most_groups(T::THREADS)) return hipErrorInvalidValue;
     return launch(w4_wide_kernel<T, PARTS>, dim3((unsigned)groups), dim3(T::THREADS), 0, s, l, p,
                   (int)wide_blocks<T>(p));
 }
@@ -726,7 +727,8 @@ hipError_t launch_w4(const W4Layout &l, const W4Problem &p, hipStream_t s) {
     const int experts = p.offsets != nullptr ? p.experts : 1;
     const int64_t each = ((int64_t)p.rows + experts - 1) / experts;
     if (each <= 2) {
-        const int64_t groups = l.strips * (p.offsets != nullptr ? most_blocks(p.rows, experts, 2) : 1);
+        const int64_t row_blocks = p.offsets != nullptr ? most_blocks(p.rows, experts, 2) : 1;
+        const int64_t groups = l.strips * row_blocks;
         return groups >= 1024 ? launch_rows<Rows<1>, 2, 2>(l, p, s)
                               : launch_rows<Rows<1>, 1, 2>(l, p, s);
     }

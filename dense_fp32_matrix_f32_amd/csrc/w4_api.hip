@@ -6,14 +6,15 @@
 #include "w4.h"
 
 using sgemm::Extent;
+using sgemm::valid_size;
 using sgemm::W4Layout;
 
 namespace {
 
 int at_least_one(int x) { return x > 1 ? x : 1; }
 
-bool valid_format(int N, int K, int group, int scale_type) {
-    return N >= 0 && K >= 0 && group > 0 &&
+bool valid_format(int experts, int N, int K, int group, int scale_type) {
+    return valid_size(experts) && valid_size(N) && valid_size(K) && group > 0 &&
            (group == 32 || group == 64 || group % sgemm::kW4Block == 0) &&
            scale_type >= SGEMM_F32_W4_SCALE_F32 && scale_type <= SGEMM_F32_W4_SCALE_BF16;
 }
@@ -58,8 +59,9 @@ hipError_t product(int rows, int N, int K, int experts, const int *offsets, cons
 
 extern "C" size_t sgemm_f32_w4_packed_size(int experts, int N, int K, int group, int scale_type,
                                            int zeros) {
-    if (experts < 0 || !valid_format(N, K, group, scale_type)) return 0;
-    const int64_t bytes = packed_bytes_of(sgemm::w4_layout(N, K, group, scale_type, zeros), experts);
+    if (!valid_format(experts, N, K, group, scale_type)) return 0;
+    const W4Layout l = sgemm::w4_layout(N, K, group, scale_type, zeros);
+    const int64_t bytes = packed_bytes_of(l, experts);
     return bytes < 0 ? 0 : (size_t)bytes;
 }
 
@@ -67,7 +69,7 @@ extern "C" hipError_t sgemm_f32_w4_pack(int experts, int N, int K, int group,
                                         const unsigned char *codes, const void *scales,
                                         int scale_type, const unsigned char *zeros, void *packed,
                                         size_t packed_bytes, hipStream_t stream) {
-    if (experts < 0 || !valid_format(N, K, group, scale_type)) return hipErrorInvalidValue;
+    if (!valid_format(experts, N, K, group, scale_type)) return hipErrorInvalidValue;
     if (experts == 0 || N == 0 || K == 0) return hipSuccess;
     const W4Layout l = sgemm::w4_layout(N, K, group, scale_type, zeros != nullptr);
     if (codes == nullptr || scales == nullptr || !valid_packed(l, experts, packed, packed_bytes) ||
@@ -87,7 +89,7 @@ extern "C" hipError_t sgemm_f32_w4_quantize(int experts, int N, int K, int group
                                             int ldb, long long strideb, int scale_type, int zeros,
                                             void *packed, size_t packed_bytes,
                                             hipStream_t stream) {
-    if (experts < 0 || !valid_format(N, K, group, scale_type) || ldb < at_least_one(N) ||
+    if (!valid_format(experts, N, K, group, scale_type) || ldb < at_least_one(N) ||
         strideb < 0)
         return hipErrorInvalidValue;
     if (experts == 0 || N == 0 || K == 0) return hipSuccess;
@@ -103,7 +105,7 @@ extern "C" hipError_t sgemm_f32_w4_unpack(int experts, int N, int K, int group, 
                                           int zeros, const void *packed, size_t packed_bytes,
                                           float *B, int ldb, long long strideb,
                                           hipStream_t stream) {
-    if (experts < 0 || !valid_format(N, K, group, scale_type) || ldb < at_least_one(N))
+    if (!valid_format(experts, N, K, group, scale_type) || ldb < at_least_one(N))
         return hipErrorInvalidValue;
     if (experts == 0 || N == 0 || K == 0) return hipSuccess;
     // one matrix must not reach into the next
@@ -120,7 +122,7 @@ extern "C" hipError_t sgemm_f32_w4_unpack(int experts, int N, int K, int group, 
 extern "C" hipError_t sgemm_f32_w4(int M, int N, int K, const float *A, int lda,
                                    const void *packed, int group, int scale_type, int zeros,
                                    float *C, int ldc, hipStream_t stream) {
-    if (M < 0 || !valid_format(N, K, group, scale_type) || lda < at_least_one(K) ||
+    if (!valid_size(M) || !valid_format(1, N, K, group, scale_type) || lda < at_least_one(K) ||
         ldc < at_least_one(N))
         return hipErrorInvalidValue;
     if (M == 0 || N == 0) return hipSuccess;
@@ -132,7 +134,7 @@ extern "C" hipError_t sgemm_f32_w4_experts(int rows, int N, int K, int experts, 
                                            const float *A, int lda, const void *packed, int group,
                                            int scale_type, int zeros, float *C, int ldc,
                                            hipStream_t stream) {
-    if (rows < 0 || experts < 0 || !valid_format(N, K, group, scale_type) ||
+    if (!valid_size(rows) || !valid_format(experts, N, K, group, scale_type) ||
         lda < at_least_one(K) || ldc < at_least_one(N))
         return hipErrorInvalidValue;
     if (rows == 0 || N == 0 || experts == 0) return hipSuccess;

@@ -19,7 +19,7 @@ from typing import NamedTuple
 import torch
 
 from ._binding import lib
-from ._tensors import INT_MAX, call, dense, matrix, place
+from ._tensors import INT_MAX, MOST, call, dense, matrix, place
 
 
 class Routing(NamedTuple):
@@ -61,7 +61,7 @@ def sort_by_expert(ids, experts, stream=None):
     ld = matrix(ids, None, None, "ids", torch.int32)
     tokens, top = ids.shape
     experts = int(experts)
-    if tokens * top > INT_MAX or not 0 <= experts < INT_MAX:
+    if tokens * top > MOST or not 0 <= experts <= MOST:
         raise ValueError(f"{tokens} x {top} pairs for {experts} experts do not fit 32-bit numbers")
     device = ids.get_device()
     offsets = ids.new_empty(experts + 1)

@@ -13,7 +13,7 @@ from __future__ import annotations
 import torch
 
 from ._binding import W4_SCALE_BF16, W4_SCALE_F16, W4_SCALE_F32, lib
-from ._tensors import INT_MAX, call, dense, matrix
+from ._tensors import INT_MAX, MOST, call, dense, matrix
 from .experts import _offsets, _stack
 
 SCALE_TYPES = {torch.float32: W4_SCALE_F32, torch.float16: W4_SCALE_F16,
@@ -41,7 +41,7 @@ def _new(experts, stacked, K, N, group, scale_dtype, zeros, device):
         raise TypeError("scales must be float32, float16 or bfloat16")
     if group not in (32, 64) and (group <= 0 or group % 128 != 0):
         raise ValueError(f"group must be 32, 64 or a multiple of 128, not {group}")
-    if max(experts, K, N, group) > INT_MAX:
+    if max(experts, K, N) > MOST or group > INT_MAX:
         raise ValueError("sizes beyond 32 bits")
     kind = SCALE_TYPES[scale_dtype]
     size = lib().sgemm_f32_w4_packed_size(experts, N, K, group, kind, int(zeros))

@@ -23,7 +23,8 @@
  * validates its arguments on the host, enqueues its kernels on `stream` and
  * returns without waiting, and a bad argument is hipErrorInvalidValue with
  * nothing enqueued: a negative size, a leading dimension below the row length, a
- * NULL buffer that would be used, a written array overlapping any other.  Sizes
+ * NULL buffer that would be used, a written array overlapping any other, a size
+ * (or tokens*top) above 2^31 - 65537, more blocks than one launch can hold.  Sizes
  * of zero enqueue nothing (unless an output still has to be written).  Calls can
  * be captured into a HIP graph.  Results are bitwise reproducible: no result
  * depends on the order in which work-groups run.
@@ -32,9 +33,10 @@
  * kernels: an expert id outside [0, experts) drops its pair; a place or pair
  * number outside its array is treated as dropped; offsets are clamped to
  * 0 <= offsets[e] <= offsets[e+1] <= rows, so no content of these arrays makes a
- * kernel leave the arrays it was given.  (Offsets whose clamped ranges overlap,
- * which sgemm_f32_route_sort() never writes, make several experts write the
- * same rows, with an unspecified result there.)
+ * kernel leave the arrays it was given.  (Offsets whose clamped ranges overlap, or
+ * a position that several pairs have, which sgemm_f32_route_sort() never writes,
+ * make several experts or pairs write the same rows, with an unspecified result
+ * there.)
  *
  * Arithmetic is IEEE fp32 with fused multiply-adds, as in sgemm_f32.h.
  */
@@ -56,7 +58,7 @@ extern "C" {
  *   order     tokens*top values: the pair at each place, by expert and, within
  *             an expert, by pair number; -1 from place offsets[experts] on.
  *   position  tokens*top values: each pair's place in `order`; -1 if dropped.
- * ldids >= max(1, top); tokens*top must fit an int.  The workspace (device
+ * ldids >= max(1, top).  The workspace (device
  * memory, 16-byte aligned, contents irrelevant before and after) must hold
  * sgemm_f32_route_workspace_size() bytes, which may be 0 (then it may be NULL);
  * calls that overlap in time must not share it.  The size is 0 for invalid

@@ -12,16 +12,19 @@
  * section "计算强度"), and W has about an eighth of the bytes of an fp32 B.
  *
  * Ownership, asynchrony and errors are those of sgemm_f32.h (bad arguments are
- * hipErrorInvalidValue with nothing enqueued; nothing is allocated and no
- * pointer kept; calls can be captured into a HIP graph).
+ * hipErrorInvalidValue with nothing enqueued, among them a size above 2^31 - 65537
+ * and more blocks than one launch can hold; nothing is allocated and no pointer
+ * kept; calls can be captured into a HIP graph).
  *
- * Arithmetic.  Sums are fp32, over products of each A[i][k] with the integers
- * q - z, which lose nothing beyond fp32 rounding; results have the accuracy of
- * an fp32 product with the fp32 matrix W.  They are bitwise reproducible for
- * fixed arguments.  A NaN or infinite A[i][k] makes all of row i NaN or infinite
- * (NaN also where the definition has an infinity); values beyond about 1e37 in
- * magnitude can overflow.  Other rows are not affected.  A zero point is taken
- * modulo 16.
+ * Arithmetic.  Sums are fp32: for each group the sum of A[i][k] * q less z times the
+ * sum of A[i][k], times s.  Rounding errors are thus relative to |A[i][k]| * s *
+ * (q + z) rather than to |q - z|, and results are as accurate as fp32 products of
+ * such terms.  The inputs enter without rounding, but bits of A[i][k] below 2^-133
+ * (1e-40) are dropped, so values from 2^-110 (8e-34) on lose nothing.  Results are
+ * bitwise reproducible for fixed arguments.  A NaN or infinite A[i][k] makes all of
+ * row i NaN or infinite (NaN also where the definition has an infinity); values
+ * beyond about 1e37 in magnitude can overflow.  Other rows are not affected.  A zero
+ * point is taken modulo 16.
  *
  * Groups.  `group` is 32, 64 or a multiple of 128 (any such value from K on
  * means one group for each column); the last group may be cut short by K.

@@ -462,6 +462,44 @@ def test_arrays_beyond_32_bits():
     assert dB[-2].eq(0).all() and dB[0].eq(0).all()
 
 
+
+def test_more_tokens_than_a_launch_has_places_for():
+    """Narrow rows of so many tokens that work-groups take several in turn."""
+    torch = torch_cuda()
+    tokens, experts = (1 << 25) + (1 << 24) + 5, 5
+    g = torch.Generator(device="cuda").manual_seed(1)
+    ids = torch.randint(-1, experts, (tokens, 1), dtype=torch.int32, device="cuda", generator=g)
+    r = sg.sort_by_expert(ids, experts)
+    kept = ids[:, 0] >= 0
+    counts = torch.bincount(ids[kept, 0], minlength=experts)
+    assert torch.equal(r.offsets[1:].long(), counts.cumsum(0))
+    x = torch.randint(-8, 9, (tokens, 1), device="cuda", generator=g).float()
+    rows = sg.gather_rows(x, r)
+    n = int(r.offsets[-1])
+    assert torch.equal(rows[:n, 0], x[r.order[:n].long(), 0])
+    w = torch.randint(-3, 4, (tokens, 1), device="cuda", generator=g).float()
+    assert torch.equal(sg.combine_rows(rows, r, w)[:, 0], torch.where(kept, w[:, 0] * x[:, 0], 0))
+    dout = torch.randint(-8, 9, (tokens, 1), device="cuda", generator=g).float()
+    drows, dw = sg.combine_rows_grad(dout, rows, r, w)
+    assert torch.equal(drows[:n, 0], (w * dout)[r.order[:n].long(), 0])
+    assert torch.equal(dw[:, 0], torch.where(kept, dout[:, 0] * x[:, 0], 0))
+
+
+def test_sort_for_millions_of_experts():
+    torch = torch_cuda()
+    experts = (1 << 22) + 17
+    ids = torch.tensor([[experts - 1, 3], [1 << 21, experts], [3, 0], [-1, (1 << 21) + 1]],
+                       dtype=torch.int32, device="cuda")
+    r = sg.sort_by_expert(ids, experts)
+    flat = ids.flatten().tolist()
+    order = sorted((f for f in range(8) if 0 <= flat[f] < experts), key=lambda f: (flat[f], f))
+    assert r.order.tolist() == order + [-1] * (8 - len(order))
+    assert r.position.flatten().tolist() == [order.index(f) if f in order else -1 for f in range(8)]
+    own = torch.tensor(sorted(flat[f] for f in order), device="cuda")
+    want = torch.searchsorted(own, torch.arange(experts + 1, device="cuda"))
+    assert torch.equal(r.offsets.long(), want)
+
+
 def test_one_matrix_for_all_experts():
     torch = torch_cuda()
     rng = np.random.default_rng(5)

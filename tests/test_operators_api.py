@@ -229,3 +229,49 @@ def test_torch_layer_refuses_tensors_of_the_host_and_of_other_types():
             f()
     with pytest.raises(TypeError):
         sg.grouped_matmul(x.double(), torch.zeros((4, 8, 8)), r.offsets)
+
+
+LARGEST = 2**31 - 65537
+
+
+@pytest.mark.parametrize("entry,base,sizes", [
+    ("sgemm_f32_route_sort", SORT, ["tokens", "experts"]),
+    ("sgemm_f32_route_gather", GATHER, ["tokens", "width"]),
+    ("sgemm_f32_route_combine", COMBINE, ["tokens", "width"]),
+    ("sgemm_f32_grouped", GROUPED, ["rows", "N", "K", "experts"]),
+    ("sgemm_f32_grouped_ta", GROUPED_TA, ["rows", "M", "N", "experts"]),
+    ("sgemm_f32_w4", W4, ["M", "N", "K"]),
+    ("sgemm_f32_w4_experts", W4E, ["rows", "N", "K", "experts"])])
+def test_sizes_that_do_not_leave_room_for_a_block_are_refused(entry, base, sizes):
+    one = {k: 1 for k in base if k in ("tokens", "top", "width", "rows", "M", "N", "K", "experts")}
+    row = {"ldids": "top", "ldw": "top", "ldx": "width", "ldrows": "width", "ldout": "width",
+           "lda": "M" if "d" in base else "K", "ldb": "N", "ldc": "N", "ldd": "N"}
+    for size in sizes:
+        for value in (LARGEST + 1, MAX):
+            # nothing else is wrong: rows as long as they must be, arrays of 8 GiB at most
+            lds = {ld: value if row[ld] == size else 1 for ld in base if ld in row}
+            _refused(entry, base, {**one, **lds, size: value}, base)
+
+
+def test_more_pairs_than_fit_are_refused():
+    pairs = {"tokens": 46341, "top": 46341}
+    _refused("sgemm_f32_route_sort", SORT, {**pairs, "ldids": 46341}, SORT)
+    _refused("sgemm_f32_route_gather", GATHER, pairs, GATHER)
+    _refused("sgemm_f32_route_combine", COMBINE, {**pairs, "ldw": 46341}, COMBINE)
+    _refused("sgemm_f32_route_combine_grad", GRAD, {**pairs, "ldw": 46341}, GRAD)
+
+
+def test_packed_size_of_sizes_that_are_refused():
+    for experts, N, K in [(LARGEST + 1, 1, 1), (1, LARGEST + 1, 1), (1, 1, LARGEST + 1)]:
+        assert sg.sgemm_f32_w4_packed_size(experts, N, K, 128, 0, 0) == 0
+    assert sg.sgemm_f32_w4_packed_size(1, 1, LARGEST, 128, 0, 0) > LARGEST // 2
+
+
+def test_more_blocks_than_a_launch_holds_are_refused():
+    far = [(i + 1) << 50 for i in range(5)]
+    # 2^24 row blocks of a work-group of 256 work-items each, and twice as many column blocks
+    rows = 1 << 29
+    assert sg.sgemm_f32_grouped(0, rows, 64, 4, rows // 32, far[0], 1.0, far[1], 4, far[2], 64, 0,
+                                0.0, far[3], 64, 0) == INVALID
+    assert sg.sgemm_f32_w4_experts(rows, 64, 128, rows // 2, far[0], far[1], 128, far[2], 128, 0, 0,
+                                   far[3], 64, 0) == INVALID

@@ -263,6 +263,28 @@ def test_small_and_large_magnitudes():
     close(run(x, w), x.astype(np.float64) @ W[0], 256, np.abs(x.astype(np.float64)) @ mag[0], "w4")
 
 
+
+@pytest.mark.parametrize("rows", [1, 5, 10, 16, 1600])
+def test_magnitudes_next_to_the_smallest(rows):
+    """Values whose last bits bf16 cannot hold: each may lose less than 2^-133, which scales of
+    2^100 lift into sight (the sums themselves are far from the smallest numbers)."""
+    torch = torch_cuda()
+    rng = np.random.default_rng(rows)
+    K, N, group = 256, 512, 64
+    for zeros in (False, True):
+        codes, s, z, W, mag = make(rng, 1, K, N, group, zeros, False, "float32")
+        w = sg.w4_pack(codes[0], s[0] * 2.0**100, None if z is None else z[0], K=K, group=group)
+        W, mag = W[0] * 2.0**100, mag[0] * 2.0**100
+        for size in (1e-33, 1e-36, 1e-38, 1e-40):
+            log(f"[gpu] w4 {rows} rows of {size}")
+            x = (rng.standard_normal((rows, K)) * size).astype(np.float32)
+            want = x.astype(np.float64) @ W
+            off = np.abs(run(x, w).double().cpu().numpy() - want)
+            limit = 1.01 * (3 * K + 8) * 2.0**-24 * (np.abs(x.astype(np.float64)) @ mag) + \
+                1.01 * 2.0**-133 * mag.sum(0)
+            assert (off <= limit).all(), (size, float((off / limit).max()))
+
+
 def quantized(B, group, zeros, scale_type):
     """The formulas of the header in fp32: the matrix that the quantised B stands for."""
     torch = torch_cuda()
