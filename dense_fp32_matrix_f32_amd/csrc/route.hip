@@ -12,6 +12,7 @@ namespace sgemm {
 namespace {
 
 typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef float f32x4_any __attribute__((ext_vector_type(4), aligned(4)));
 
 // ---------------------------------------------------------------------------
 // The order: a counting sort by expert, stable in f.  Dropped pairs count as one
@@ -29,7 +30,10 @@ typedef float f32x4 __attribute__((ext_vector_type(4)));
 // a launch.
 constexpr int kSortThreads = 1024, kSortWaves = kSortThreads / 64;
 constexpr int kSortChunks = 128;         // at most
-constexpr int kSortBuckets = 896;        // experts + 1 at most (56 KB of LDS)
+constexpr int kSortBuckets = 896;        // experts + 1 at most (63 KB of LDS)
+
+// Work-items that add up the counts of one bucket.
+__host__ __device__ constexpr int sort_slices(int buckets) { return kSortThreads / buckets; }
 
 struct SortArgs {
     Pairs p;
@@ -80,6 +84,28 @@ __global__ __launch_bounds__(kSortThreads) void sort_place_kernel(SortArgs a, in
     __shared__ int sums[kSortWaves];
     const int buckets = a.experts + 1;
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    // the chunks' counts of a bucket, before this chunk and all, added by `slices`
+    // work-items, each over every slices-th chunk
+    int *parts = next + kSortWaves * buckets;  // [slice][bucket] of each
+    const int slices = sort_slices(buckets);
+    if (a.counts != nullptr && tid < slices * buckets) {
+        const int slice = tid / buckets, *c = a.counts + tid % buckets;
+        int before = 0, all = 0;
+        for (int b0 = slice; b0 < a.chunks; b0 += 16 * slices) {
+            int v[16];  // loads without a branch, so that all are in flight
+#pragma unroll
+            for (int u = 0; u < 16; ++u)
+                v[u] = c[(int64_t)min(b0 + u * slices, a.chunks - 1) * buckets];
+#pragma unroll
+            for (int u = 0; u < 16; ++u) {
+                const int b = b0 + u * slices;
+                if (b < (int)blockIdx.x) before += v[u];
+                if (b < a.chunks) all += v[u];
+            }
+        }
+        parts[tid] = before;
+        parts[slices * buckets + tid] = all;
+    }
     for (int i = tid; i < buckets * kSortWaves; i += kSortThreads) next[i] = 0;
     __syncthreads();
     const Run run(a);
@@ -91,12 +117,9 @@ __global__ __launch_bounds__(kSortThreads) void sort_place_kernel(SortArgs a, in
     int before = 0, all = 0;
     if (tid < buckets) {
         if (a.counts != nullptr) {
-            const int *c = a.counts + tid;
-#pragma unroll 8
-            for (int b = 0; b < a.chunks; ++b) {
-                const int v = c[(int64_t)b * buckets];
-                if (b < (int)blockIdx.x) before += v;
-                all += v;
+            for (int i = 0; i < slices; ++i) {
+                before += parts[i * buckets + tid];
+                all += parts[(slices + i) * buckets + tid];
             }
         } else {
             for (int w = 0; w < kSortWaves; ++w) all += next[w * buckets + tid];
@@ -195,10 +218,11 @@ void sort_cut(int64_t n, int *run, int *chunks) {
 // ---------------------------------------------------------------------------
 // Rows there and back.  The lanes of a row take four columns each (16-byte accesses,
 // which gfx950 takes at any multiple of four bytes).  8192 tokens of 2048 columns with
-// four choices each: gather 54 us (335 MB, 6.2 TB/s, mostly written), combine 89 us
-// (335 MB, 3.8 TB/s, mostly read; a sum over 2 GiB reads 4.0), the gradients 113 us (603 MB, 5.3
-// TB/s; a copy of 2 GiB reaches 5.0).  Two column vectors of a lane in flight instead of one left
-// combine at 89 us.
+// four choices each: gather 56 us (335 MB, 6.0 TB/s, mostly written), combine 58 us (335
+// MB, 5.8 TB/s, mostly read), the gradients 128 us (603 MB, 4.7 TB/s; a copy of 2 GiB
+// reaches 5.0); what one kernel leaves in the last cache to be written back is part of
+// the next one's time, so the four calls of a step together count: 301 us.  Two column
+// vectors of a lane in flight instead of one changed nothing.
 
 // Work-items for a row: enough for its vectors, a power of two from 16 to `most`.
 int lanes_for(int width, int most) {
@@ -206,14 +230,6 @@ int lanes_for(int width, int most) {
     while (lanes < most && lanes * 4 < width) lanes *= 2;
     return lanes;
 }
-
-__device__ __forceinline__ f32x4 load4(const float *p) {
-    f32x4 v;
-    __builtin_memcpy(&v, p, 16);
-    return v;
-}
-
-__device__ __forceinline__ void store4(float *p, f32x4 v) { __builtin_memcpy(p, &v, 16); }
 
 // Calls body(c, vector) for this lane's columns of [begin, end): with 16-byte vectors
 // at c, then for the last end % 4 columns one by one on the first lanes.
@@ -228,10 +244,24 @@ __device__ __forceinline__ void for_columns(int64_t begin, int64_t end, int lane
 template <bool VECTOR>
 using Cols = typename std::conditional<VECTOR, f32x4, float>::type;
 
-__device__ __forceinline__ f32x4 load(const float *p, std::true_type) { return load4(p); }
+__device__ __forceinline__ f32x4 load(const float *p, std::true_type) {
+    return *(const f32x4_any *)p;
+}
 __device__ __forceinline__ float load(const float *p, std::false_type) { return *p; }
-__device__ __forceinline__ void store(float *p, f32x4 v) { store4(p, v); }
-__device__ __forceinline__ void store(float *p, float v) { *p = v; }
+template <bool PAST = false>
+__device__ __forceinline__ void store(float *p, f32x4 v) {
+    if constexpr (PAST)
+        __builtin_nontemporal_store((f32x4_any)v, (f32x4_any *)p);
+    else
+        *(f32x4_any *)p = v;
+}
+template <bool PAST = false>
+__device__ __forceinline__ void store(float *p, float v) {
+    if constexpr (PAST)
+        __builtin_nontemporal_store(v, p);
+    else
+        *p = v;
+}
 __device__ __forceinline__ f32x4 mul_add(float w, f32x4 v, f32x4 sum) {
     for (int e = 0; e < 4; ++e) sum[e] = fmaf(w, v[e], sum[e]);
     return sum;
@@ -242,6 +272,16 @@ __device__ __forceinline__ float dot_add(f32x4 a, f32x4 b, float sum) {
     return sum;
 }
 __device__ __forceinline__ float dot_add(float a, float b, float sum) { return fmaf(a, b, sum); }
+
+// Loads of what is read once, past the caches: gather, combine, gradients and combine
+// of 4096 tokens of 2048 columns with four choices 155 -> 146 us, of 8192 tokens 339 ->
+// 268 with buffers allocated once and 339 -> 326 with new ones.
+__device__ __forceinline__ f32x4 load_once(const float *p, std::true_type) {
+    return __builtin_nontemporal_load((const f32x4_any *)p);
+}
+__device__ __forceinline__ float load_once(const float *p, std::false_type) {
+    return __builtin_nontemporal_load(p);
+}
 
 constexpr int J = 4;  // choices whose loads are in flight together
 
@@ -286,7 +326,23 @@ __global__ __launch_bounds__(256) void gather_kernel(Pairs p, int width, int lan
         }
 }
 
+// Whether results are stored past the caches too: where the rows alone fill the last
+// cache (256 MB), so that what is written takes the place of what is still to be read.
+// The four calls above, in us:
+//                                                        cached  past
+//   8192 tokens of 2048, four choices (268 MB), new buffers  326   301
+//   the same, buffers allocated once                         265   282
+//   9000 tokens of 2048, four choices                        289   312
+//   8192 tokens of 4096, two choices                         389   367
+//   16384 tokens of 2048, four choices                       597   589
+//   32768 tokens of 2048, eight choices                     2370  2251
+//   4096 tokens of 2048, four choices (134 MB)               146   165
+bool store_past(Pairs p, int width) {
+    return (int64_t)p.count() * width * 4 >= (int64_t)256 << 20;
+}
+
 // out[t] = sum of weights[t, j] * rows[position[t, j]] in the order of j.
+template <bool PAST>
 __global__ __launch_bounds__(256) void combine_kernel(Pairs p, int width, int lanes, int span,
                                                       const int *__restrict__ position,
                                                       const float *__restrict__ weights,
@@ -303,14 +359,14 @@ __global__ __launch_bounds__(256) void combine_kernel(Pairs p, int width, int la
             auto add = [&](const Choices &k) {
                 Cols<decltype(vector)::value> v[J];
 #pragma unroll
-                for (int j = 0; j < J; ++j) v[j] = load(rows + k.row(j) * ldrows + c, vector);
+                for (int j = 0; j < J; ++j) v[j] = load_once(rows + k.row(j) * ldrows + c, vector);
 #pragma unroll
                 for (int j = 0; j < J; ++j)
                     if (k.place[j] >= 0) sum = mul_add(k.w[j], v[j], sum);
             };
             if (p.top > 0) add(first);
             for (int j0 = J; j0 < p.top; j0 += J) add(Choices(p, t, j0, position, weights, ldw));
-            store(out + t * ldout + c, sum);
+            store<PAST>(out + t * ldout + c, sum);
         });
     }
 }
@@ -318,6 +374,7 @@ __global__ __launch_bounds__(256) void combine_kernel(Pairs p, int width, int la
 // The gradients of a token, four choices at a time: its dout is read once for them;
 // a choice's product with its row is added over the lanes in a fixed order (a
 // butterfly in each wave, then the waves in turn).
+template <bool PAST>
 __global__ __launch_bounds__(1024) void combine_grad_kernel(
     Pairs p, int width, int lanes, const int *__restrict__ position,
     const float *__restrict__ weights, int64_t ldw, const float *__restrict__ rows, int64_t ldrows,
@@ -340,7 +397,7 @@ __global__ __launch_bounds__(1024) void combine_grad_kernel(
                         V y[J];
 #pragma unroll
                         for (int j = 0; j < J; ++j)
-                            y[j] = load(rows + k.row(j) * ldrows + c, vector);
+                            y[j] = load_once(rows + k.row(j) * ldrows + c, vector);
 #pragma unroll
                         for (int j = 0; j < J; ++j)
                             if (k.place[j] >= 0) dot[j] = dot_add(g, y[j], dot[j]);
@@ -349,7 +406,7 @@ __global__ __launch_bounds__(1024) void combine_grad_kernel(
 #pragma unroll
                         for (int j = 0; j < J; ++j)
                             if (k.place[j] >= 0)
-                                store(drows + k.place[j] * lddrows + c, k.w[j] * g);
+                                store<PAST>(drows + k.place[j] * lddrows + c, k.w[j] * g);
                     }
                 });
             }
@@ -411,16 +468,18 @@ hipError_t launch_route_sort(Pairs p, int experts, const int *ids, int64_t ldids
     if (experts >= kSortBuckets)
         return launch(sort_each_kernel, dim3(route_groups((int64_t)experts + 1)),
                       dim3(kSortThreads), 0, s, a, offsets, order, position);
+    const int buckets = experts + 1;
+    size_t lds = sizeof(int) * kSortWaves * (size_t)buckets;
     if (a.chunks == 1) {
         a.counts = nullptr;
     } else {
+        lds += 2 * sizeof(int) * sort_slices(buckets) * (size_t)buckets;
         const hipError_t e = launch(sort_count_kernel, dim3((unsigned)a.chunks),
                                     dim3(kSortThreads), 0, s, a);
         if (e != hipSuccess) return e;
     }
-    return launch(sort_place_kernel, dim3((unsigned)a.chunks), dim3(kSortThreads),
-                  sizeof(int) * kSortWaves * (size_t)(experts + 1), s, a, offsets, order,
-                  position);
+    return launch(sort_place_kernel, dim3((unsigned)a.chunks), dim3(kSortThreads), lds, s, a,
+                  offsets, order, position);
 }
 
 hipError_t launch_route_gather(Pairs p, int width, const int *position, const float *x,
@@ -440,8 +499,9 @@ hipError_t launch_route_combine(Pairs p, int width, const int *position, const f
     const int64_t groups = ((int64_t)p.tokens * lanes + 255) / 256;
     const int span = span_for(groups, width, lanes);
     const dim3 grid(route_groups(groups), (unsigned)(((int64_t)width + span - 1) / span));
-    return launch(combine_kernel, grid, dim3(256), 0, s, p, width, lanes, span, position, weights,
-                  ldw, rows, ldrows, out, ldout);
+    return launch(store_past(p, width) ? combine_kernel<true> : combine_kernel<false>, grid,
+                  dim3(256), 0, s, p, width, lanes, span, position, weights, ldw, rows, ldrows, out,
+                  ldout);
 }
 
 hipError_t launch_route_combine_grad(Pairs p, int width, const int *position,
@@ -453,9 +513,9 @@ hipError_t launch_route_combine_grad(Pairs p, int width, const int *position,
     const int lanes = lanes_for(width, p.tokens < 512 ? 1024 : 256);
     const int threads = lanes > 256 ? lanes : 256;
     const int64_t groups = ((int64_t)p.tokens * lanes + threads - 1) / threads;
-    return launch(combine_grad_kernel, dim3(route_groups(groups)), dim3((unsigned)threads), 0, s, p,
-                  width, lanes, position, weights, ldw, rows, ldrows, dout, lddout, drows,
-                  lddrows, dweights);
+    return launch(store_past(p, width) ? combine_grad_kernel<true> : combine_grad_kernel<false>,
+                  dim3(route_groups(groups)), dim3((unsigned)threads), 0, s, p, width, lanes,
+                  position, weights, ldw, rows, ldrows, dout, lddout, drows, lddrows, dweights);
 }
 
 }  // namespace sgemm
