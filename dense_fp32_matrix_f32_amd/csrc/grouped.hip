@@ -9,6 +9,9 @@ namespace sgemm {
 
 namespace {
 
+typedef float f32x4_any __attribute__((ext_vector_type(4), aligned(4)));
+constexpr int kFewRows = 16, kFewCols = 64;  // a block of grouped_few_kernel
+
 // Blocks of C.  Row blocks are counted expert by expert (find_block); the launch
 // holds the most there can be, and the work-groups past those there are leave at
 // once.  The ones there are get the XCD-aware order of the plain product, over all
@@ -38,6 +41,137 @@ __global__ __launch_bounds__(C::THREADS, C::OCC) void grouped_kernel(GroupedProb
     mma_tile<C>(g, lds, m0, n0, 0, (g.K + C::BK - 1) / C::BK, acc);
     const int r_first = KwReduce<C>::run(lds, acc);
     store_tile<C>(g, m0, n0, acc, 0, n_lo, r_first, KwReduce<C>::RPG);
+}
+
+// Few rows of each expert: bound by reading the matrices once.  A work-group forms up
+// to 16 rows by 64 columns; its eight waves take units of 32 k in turn and their sums
+// are added at the end, in a fixed order.  Operands go from memory to the 16x16x4
+// matrix instruction without LDS: lane group q = lane / 16 holds k = 4q .. 4q+3 of
+// each 16, so a 16-byte load is a row of A, or of a transposed B, for four
+// instructions; of B as given it is four columns of one k, one for each of four
+// instructions whose columns are 4i + e (i = lane % 16, e = the instruction).  B as given
+// is loaded past the caches, a unit at a time (48 rows, 8 experts of 2048 x 4096: 45.7
+// us, 5.9 TB/s; through the caches 51.9; two units in flight 48.6, three 54.6, with
+// fewer waves).  B transposed is loaded by halves of a cache line and keeps its place
+// in the caches, two units in flight (53.5 us; past the caches 62; one unit 57 to 72).
+template <bool TB>
+__global__ __launch_bounds__(512) void grouped_few_kernel(GroupedProblem p, int row_blocks) {
+    constexpr int W = 8, COLS = kFewCols, UNIT = 32;
+    __shared__ float red[W][kFewRows][COLS + 1];
+    const int lane = threadIdx.x & 63, q = lane >> 4, i = lane & 15;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    // row blocks of one expert and strip follow each other: they share its B in one L2
+    const unsigned id = xcd_remap(blockIdx.x, gridDim.x);
+    const int n0 = id / (unsigned)row_blocks * COLS;
+    int expert, first, end;
+    if (!find_block(p.offsets, p.experts, p.rows, kFewRows, id % (unsigned)row_blocks, &expert,
+                    &first, &end))
+        return;
+    const int rows = min(kFewRows, end - first);
+    const float *a = p.A + (int64_t)(first + min(i, rows - 1)) * p.lda + 4 * q;
+    const float *mat = p.B + expert * p.strideb;
+    // this lane's columns: n0 + 16u + i (B transposed), or four from `col` on, which at
+    // the right edge are the last four
+    const int col = TB ? 0 : min(n0 + 4 * i, p.N - 4);
+    const float *b[4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u)
+        b[u] = TB ? mat + (int64_t)min(n0 + 16 * u + i, p.N - 1) * p.ldb + 4 * q
+                  : mat + (int64_t)(4 * q + u) * p.ldb + col;
+
+    struct Unit {
+        f32x4 a[2], b[2][4];
+    };
+    auto load = [&](Unit &x, int unit) {
+        const int64_t k = (int64_t)unit * UNIT;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            x.a[h] = load16(a + k + 16 * h);
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                const float *from = b[u] + (TB ? k + 16 * h : (k + 16 * h) * p.ldb);
+                x.b[h][u] = TB ? load16(from)
+                               : __builtin_nontemporal_load((const f32x4_any *)from);
+            }
+        }
+    };
+    f32x4 acc[4] = {};
+    auto multiply = [&](const Unit &x) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    acc[e] = __builtin_amdgcn_mfma_f32_16x16x4f32(
+                        x.a[h][j], TB ? x.b[h][e][j] : x.b[h][j][e], acc[e], 0, 0, 0);
+    };
+
+    // Units wave, wave + W, ..., the loads of the next D always issued before one is used
+    // (past the last they repeat it).  With B transposed the rows of all strips would start
+    // on the same memory channels, so strips start a pass of the waves apart.
+    const int units = p.K / UNIT, n = (units - wave + W - 1) / W;
+    if (n > 0) {
+        constexpr int D = TB ? 2 : 1;
+        const int rot = TB ? (int)(id / (unsigned)row_blocks * W % (unsigned)units) : 0;
+        auto at = [&](int t) {
+            const int unit = wave + min(t, n - 1) * W + rot;
+            return unit >= units ? unit - units : unit;
+        };
+        Unit x[D];
+#pragma unroll
+        for (int u = 0; u < D; ++u) load(x[u], at(u));
+        int t = 0;
+        for (; t + D < n; t += D) {
+#pragma unroll
+            for (int u = 0; u < D; ++u) {
+                multiply(x[u]);
+                load(x[u], at(t + u + D));
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < D; ++u)
+            if (t + u < n) multiply(x[u]);
+    }
+    // the last k, fewer than a unit
+    if (p.K % UNIT != 0 && wave == units % W) {
+        const int k0 = units * UNIT;
+        Unit x;
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int k = k0 + 16 * h + j;  // and 4q more
+                const bool in = k + 4 * q < p.K;
+                x.a[h][j] = in ? a[k] : 0.0f;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    if constexpr (TB)
+                        x.b[h][e][j] = in ? b[e][k] : 0.0f;
+                    else
+                        x.b[h][j][e] = in ? b[j][(int64_t)(k - j) * p.ldb + e] : 0.0f;
+                }
+            }
+        multiply(x);
+    }
+
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        const int at = TB ? 16 * e + i : col + e - n0;
+        if (!TB && at < 4 * i) continue;  // another lane's column
+#pragma unroll
+        for (int r = 0; r < 4; ++r) red[wave][4 * q + r][at] = acc[e][r];
+    }
+    __syncthreads();
+    for (int o = threadIdx.x; o < rows * COLS; o += 64 * W) {
+        const int m = o / COLS, c = o % COLS;
+        if (n0 + c >= p.N) continue;
+        float sum = 0.0f;
+#pragma unroll
+        for (int w = 0; w < W; ++w) sum += red[w][m][c];
+        float *dst = p.C + (int64_t)(first + m) * p.ldc + n0 + c;
+        *dst = epilogue(sum, p.alpha, p.beta, dst);
+    }
 }
 
 // Blocks of every C_e; the k loop of a block runs over its expert's rows.  Each
@@ -96,6 +230,15 @@ hipError_t launch_blocks(const GroupedProblem &p, hipStream_t s) {
                   (int)tiles_n);
 }
 
+template <bool TB>
+hipError_t launch_few(const GroupedProblem &p, hipStream_t s) {
+    const int64_t row_blocks = most_blocks(p.rows, p.experts, kFewRows);
+    const int64_t groups = ((int64_t)p.N + kFewCols - 1) / kFewCols * row_blocks;
+    if (groups > most_groups(512)) return hipErrorInvalidValue;
+    return launch(grouped_few_kernel<TB>, dim3((unsigned)groups), dim3(512), 0, s, p,
+                  (int)row_blocks);
+}
+
 // Configuration T of the plain product with R register sets; rows so long that an
 // offset inside a block passes 31 bits take 64-bit addresses (on one configuration).
 template <class T, bool TB, int R>
@@ -135,15 +278,27 @@ hipError_t launch_grouped_ta_tile(const GroupedTaProblem &p, hipStream_t s) {
 //  16384, 4, 4096 x 4096   4768 / 4769 4179 / 4300 3932 / 3945 3848 / 3888
 // (the first two rows against 54 and 27 us to read the matrices at 5 TB/s, the last two
 // against 893 and 3570 us at the 154 TFLOP/s of a large plain product).  32 x 32 blocks
-// with B as given: one register set is faster for the fewest rows (48 rows: 55 against
-// 65, 512 rows 33 against 38), two for more (400 rows: 95 against 110).
+// with B as given have one register set for few rows on many work-groups, two else; the
+// kernel for few rows needs the many work-groups too, whether B is transposed or not:
+//   rows, experts, N x K       few rows   one set / two / transposed
+//     48,  8, 4096 x 2048       46 / 54    55 /  69 /  65
+//     80,  8, 4096 x 2048       58 / 74    58 /  72 /  69
+//    200,  8, 4096 x 2048       80 / 89     - /  71 /  67
+//    512, 64, 1024 x  512       28 / 32    33 /  44 /  37
+//    400, 64, 2048 x 1024       93 / 108    - / 126 / 122
+//    256, 16, 2048 x 2048       62 / 74    60 /  75 /  68
+//     48,  8, 2048 x 2048       32 / 45    44 /  32 /  34   (one work-group a CU)
+//      4,  1, 4096 x 4096       29 / 35    43 /  27 /  26
 template <bool TB>
 hipError_t launch_grouped_as(const GroupedProblem &p, hipStream_t s) {
     const int each = p.rows / p.experts;
     if (each >= 4096) return launch_grouped_tile<TileTall, TB, 1>(p, s);
     if (each > 64) return launch_grouped_tile<TileSmall, TB, 3>(p, s);
-    if constexpr (!TB) {
-        if (each <= 16) return launch_grouped_tile<TileTiny, TB, 1>(p, s);
+    if (((int64_t)p.N + kFewCols - 1) / kFewCols * p.experts >= 2 * compute_units()) {
+        if (each <= 8 && p.N >= 4) return launch_few<TB>(p, s);
+        if constexpr (!TB) {
+            if (each <= 16) return launch_grouped_tile<TileTiny, TB, 1>(p, s);
+        }
     }
     return launch_grouped_tile<TileTiny, TB, 2>(p, s);
 }

@@ -25,7 +25,7 @@ typedef float f32x4_any __attribute__((ext_vector_type(4), aligned(4)));
 // its run 64 pairs at a time, a pair's rank among equal ones found by comparing
 // the bits of its expert with ballots.  With more than one chunk a first kernel
 // leaves every chunk's counts in the workspace.  No place depends on which
-// work-group or wave runs first.  262144 pairs for 256 experts: 3.2 + 12.2 us (one
+// work-group or wave runs first.  262144 pairs for 256 experts: 3.3 + 11.2 us (one
 // work-group for each expert, walking all pairs: 344 us); eight pairs: 2.6 us, the time of
 // a launch.
 constexpr int kSortThreads = 1024, kSortWaves = kSortThreads / 64;

@@ -216,7 +216,10 @@ def plain_grouped(A, B, offsets, C, alpha, beta):
 
 SHAPES = [(1, 1, 1, 1), (1, 8, 8, 3), (5, 17, 33, 2), (16, 64, 64, 4), (65, 130, 100, 3),
           (200, 96, 257, 5), (333, 257, 63, 70), (130, 4, 500, 4), (64, 1000, 2, 2),
-          (700, 200, 72, 8), (48, 520, 1040, 16)]
+          (700, 200, 72, 8), (48, 520, 1040, 16),
+          # few rows of each of many experts
+          (300, 257, 70, 200), (700, 1000, 33, 100), (1000, 5, 130, 600), (500, 68, 1, 300),
+          (2000, 130, 64, 256)]
 
 
 @pytest.mark.parametrize("groups", list(GROUPS))
@@ -256,6 +259,31 @@ def test_grouped(rows, N, K, experts, groups):
             close(dC, want, K, mag, "grouped")
         dC[:] = SENT
         assert int((buf != SENT).sum()) == 0, "wrote outside C"
+
+
+
+@pytest.mark.parametrize("trans", [False, True])
+@pytest.mark.parametrize("rows,N,K,experts", [(200, 300, 33, 150), (200, 300, 40, 150), (9, 20, 33, 3)])
+def test_grouped_values_that_are_not_finite(rows, N, K, experts, trans):
+    """An infinity in the last row of a matrix, or in the first row of the next one, is met only by
+    the values of A that belong to it; one in A stays in its row."""
+    torch = torch_cuda()
+    rng = np.random.default_rng(K)
+    offsets = GROUPS["uneven"](rows, experts) if "uneven" in GROUPS else \
+        np.sort(np.concatenate([[0], rng.integers(0, rows + 1, experts - 1), [rows]]))
+    A, B = int_matrix(rng, rows, K), int_matrix(rng, experts, K, N)
+    A[:, K - 1] = 1.0
+    B[1::3, K - 1, N // 2] = np.inf
+    B[1::3, 0, N - 1] = -np.inf
+    A[:, 0] = 2.0
+    A[rows // 2, K // 2] = np.nan
+    dB = torch.from_numpy(np.ascontiguousarray(B.transpose(0, 2, 1)) if trans else B).cuda()
+    got = sg.grouped_matmul(torch.from_numpy(A).cuda(), dB.transpose(1, 2) if trans else dB,
+                            torch.from_numpy(offsets.astype(np.int32)).cuda()).cpu().numpy()
+    for e, (lo, hi) in enumerate(zip(offsets, offsets[1:])):
+        for i in range(lo, hi):
+            want = (A[i][:, None].astype(np.float64) * B[e]).sum(0)
+            assert np.array_equal(got[i].astype(np.float64), want, equal_nan=True), (e, i)
 
 
 @pytest.mark.parametrize("rows,N,K,experts", [(9001, 200, 330, 2), (620, 130, 1030, 4),
