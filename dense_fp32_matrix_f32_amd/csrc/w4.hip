@@ -416,7 +416,7 @@ hipError_t launch_rows(const W4Layout &l, const W4Problem &p, hipStream_t s) {
 // ---------------------------------------------------------------------------
 // Many rows.  Cutting A into parts costs about six vector operations a value, and
 // in the kernel above every work-group cuts its rows for 16 to 64 columns only.
-// Here a work-group computes 16 or 32 rows by 256 or 512 columns over all k, its waves
+// Here a work-group computes 16 or 32 rows by 128 to 512 columns over all k, its waves
 // side by side in columns, and A is cut once for all of them, into two stages of LDS:
 // while one block of 128 k is multiplied, the next one's x is cut, one barrier a block.
 // The sums of A over 32 k (for the zero points) are formed on the way, in fp32.
@@ -660,31 +660,50 @@ hipError_t launch_wide(const W4Layout &l, const W4Problem &p, hipStream_t s) {
                   (int)wide_blocks<T>(p));
 }
 
-// 16 rows by 256 columns, or 32 by 512 (32 by 256 with four scales of a column in a
-// block, which need more registers than the larger leaves).  A larger block cuts A for
-// more columns and unpacks codes for more rows; it is taken where it still gives every
-// CU a work-group (two of the middle one).  Times in us:
-//                                          16 x 256  32 x 256  32 x 512
-//   256 rows 4096 x 4096, group 128          33        51
-//   1000 rows by expert, 16 x 2048 x 2048    47        58
-//   512 rows 4096 x 4096, group 32           66        65       252
-//   512 rows 8192 x 4096, group 128         100        94        88
-//   2048 rows 4096 x 4096, group 64         220       225       191
-using Wide16 = Wide<8, 1, 2, 2>;
-using Wide256 = Wide<8, 2, 2, 2>;
-using Wide512 = Wide<8, 2, 4, 2>;
+// 16 rows by 128 or 256 columns, or 32 by 512 (32 by 256 with four scales of a column
+// in a block, which need more registers than the larger leaves).  A larger block cuts A
+// for more columns and unpacks codes for more rows, but fewer of them fill the CUs less
+// evenly and waste more of an expert's last one.  So the largest is taken where its
+// rounds over the CUs are at least four fifths full (for experts, from 512 rows each on),
+// and of the others 16 by 256 where it nearly fills the CUs and is not just past that.
+// With four scales 16 by 256 gains nothing over 16 by 128.  Times in us:
+//                                          16 x 128  16 x 256  largest
+//   128 rows 4096 x 4096, group 64           26        37
+//   256 rows 4096 x 4096, group 128          36        33        85
+//   320 rows 4096 x 4096, group 64           51        56        93
+//   700 rows 4096 x 4096, group 128          96        80        86
+//   512 rows 8192 x 4096, group 128         133       109        88
+//   1024 rows 4096 x 4096, group 64         141       119        95
+//   512 rows by expert, 16 x 2048 x 2048     28        31
+//   1000 rows by expert, 64 x 2048 x 1024    30        26        50
+//   2048 rows by expert, 8 x 4096 x 2048    145       121       134
+//   4096 rows by expert, 8 x 4096 x 2048    283       237       224
+//   300 rows 4096 x 4096, group 32           62        79        64
+//   512 rows 4096 x 4096, group 32           82        81        65
+//   700 rows 4096 x 4096, group 32          117       119       126
+//   256 by expert, 16 x 1408 x 4096, 32      42        41        64
+//   2000 by expert, 16 x 1408 x 4096, 32    124       160       128
+using Wide128 = Wide<8, 1, 1, 2>;
+using Wide256 = Wide<8, 1, 2, 2>;
 
 template <int PARTS>
 hipError_t launch_wide_as(const W4Layout &l, const W4Problem &p, hipStream_t s) {
-    using Large = typename std::conditional<PARTS == 4, Wide256, Wide512>::type;
-    const int least = (PARTS == 4 ? 2 : 1) * compute_units();
-    return wide_groups<Large>(l, p) >= least ? launch_wide<Large, PARTS>(l, p, s)
-                                             : launch_wide<Wide16, PARTS>(l, p, s);
+    using Largest = typename std::conditional<PARTS == 4, Wide<8, 2, 2, 2>, Wide<8, 2, 4, 2>>::type;
+    const int64_t cus = compute_units();
+    const int64_t largest = wide_groups<Largest>(l, p), rounds = (largest + cus - 1) / cus;
+    if (5 * largest >= 4 * cus * rounds && (p.offsets == nullptr || p.rows / p.experts >= 512))
+        return launch_wide<Largest, PARTS>(l, p, s);
+    if constexpr (PARTS < 4) {
+        const int64_t groups = wide_groups<Wide256>(l, p);
+        if (groups >= cus * 5 / 8 && (groups <= cus || groups > cus * 3 / 2))
+            return launch_wide<Wide256, PARTS>(l, p, s);
+    }
+    return launch_wide<Wide128, PARTS>(l, p, s);
 }
 
 // Whether there are rows enough for these kernels, and their offsets fit.
 bool many_rows(const W4Layout &l, const W4Problem &p) {
-    return wide_groups<Wide16>(l, p) >= compute_units() && wide_fits<Wide512>(l, p);
+    return wide_groups<Wide128>(l, p) >= compute_units() && wide_fits<Wide<8, 2, 4, 2>>(l, p);
 }
 
 hipError_t launch_many_rows(const W4Layout &l, const W4Problem &p, hipStream_t s) {
@@ -709,9 +728,11 @@ hipError_t launch_many_rows(const W4Layout &l, const W4Problem &p, hipStream_t s
 //   16    4096 x 4096, 128  one strip 9.7    two 10.2, four 13.0; 10-row form 9.7
 //   16    8192 x 8192, 64   two strips 19.1  one 32.8, four 24.6
 //   32    4096 x 4096, 128  two strips 10.6  one 17.2, four 13.5
-//   256 by expert, 16 x 1408 x 4096, 32: two strips 38.8, one 58, four 44
+//   256 by expert, 16 x 1408 x 4096, 32: many rows 42, two strips 44, one 64, four 49
+//   256 by expert, 16 x 2048 x 2048, 128: many rows 19, two strips 26
 //   64    4096 x 4096, 128  four strips 14.1 two 18.9; many rows 32
-//   128   4096 x 4096, 64   four strips 27.0 two 35.2; many rows 36
+//   128   4096 x 4096, 64   many rows 25.6   four strips 27.0, two 35.2
+//   128   8192 x 4096, 128  many rows 33.2   four strips 32.9
 //   256   4096 x 4096, 128  many rows 33     four strips 49
 //   512   4096 x 4096, 32   many rows 65     four strips 121
 //   512   8192 x 4096, 128  many rows 88     four strips 197

@@ -112,10 +112,12 @@ def test_product_of_ordinary_sizes(rows, N, K):
 
 
 @pytest.mark.parametrize("rows,N,K,group", [
-    (1000, 1500, 300, 32), (1001, 1500, 300, 256), (801, 2047, 129, 64),   # 16 x 256
-    (4100, 1000, 300, 32), (4111, 1023, 140, 32),                          # 32 x 256
-    (2100, 2000, 200, 64), (2081, 1999, 385, 256),                         # 32 x 512
-    (513, 2900, 1030, 128), (6200, 256, 4, 32)])
+    (1000, 1500, 300, 32), (4100, 1000, 300, 32), (4111, 1023, 140, 32), (6200, 256, 4, 32),
+    (1001, 1500, 300, 256), (600, 2047, 129, 64),                          # 16 x 128
+    (801, 2047, 129, 64), (2100, 2000, 200, 64), (2081, 1999, 385, 256),
+    (513, 2900, 1030, 128),                                                # 16 x 256
+    (1001, 2047, 140, 32), (2030, 1000, 300, 32),                          # 32 x 256
+    (2048, 2000, 200, 64), (2019, 1999, 385, 256)])                        # 32 x 512
 def test_product_of_many_rows(rows, N, K, group):
     """Sizes at which the kernels for many rows run, from one work-group a CU on."""
     torch = torch_cuda()
@@ -135,13 +137,15 @@ def test_product_of_many_rows(rows, N, K, group):
 
 
 @pytest.mark.parametrize("which", ["one has all", "ragged", "rows of no expert"])
-def test_product_of_many_rows_by_expert(which):
+@pytest.mark.parametrize("rows,N,experts,group", [(1000, 1300, 16, 64), (500, 1300, 16, 128),
+                                                  (2200, 1500, 4, 64), (2200, 700, 4, 32)])
+def test_product_of_many_rows_by_expert(rows, N, experts, group, which):
     torch = torch_cuda()
-    rows, N, K, experts = 1000, 1300, 200, 16
+    K = 200
     rng = np.random.default_rng(5)
     offsets = [int(o) for o in OFFSETS[which](rows, experts)]
-    codes, s, z, W, mag = make(rng, experts, K, N, 64, True, True, "float16")
-    w = sg.w4_pack(codes, s, z, K=K, group=64)
+    codes, s, z, W, mag = make(rng, experts, K, N, group, True, True, "float16")
+    w = sg.w4_pack(codes, s, z, K=K, group=group)
     x = rng.integers(-4, 5, (rows, K)).astype(np.float32)
     got = run(x, w, offsets=torch.tensor(offsets, dtype=torch.int32, device="cuda"), pad=3)
     want = np.full((rows, N), SENT)
