@@ -12,23 +12,11 @@ namespace {
 typedef float f32x4_any __attribute__((ext_vector_type(4), aligned(4)));
 constexpr int kFewRows = 16, kFewCols = 64;  // a block of grouped_few_kernel
 
-// Blocks of C.  Row blocks are counted expert by expert (find_block); the launch
-// holds the most there can be, and the work-groups past those there are leave at
-// once.  The ones there are get the XCD-aware order of the plain product, over all
-// experts' row blocks: those of one expert follow each other and share its matrix.
+// One block of C: rows from `first` on of expert e, whose rows end at `end`, and column
+// block tn.
 template <class C>
-__global__ __launch_bounds__(C::THREADS, C::OCC) void grouped_kernel(GroupedProblem p,
-                                                                    int tiles_n) {
-    __shared__ __attribute__((aligned(16))) float lds[C::LDS_FLOATS];
-    // (offsets that are no running sum can give more blocks than were launched, or a
-    // count that wrapped to a negative one)
-    const int tiles_m = min(count_blocks(p.offsets, p.experts, p.rows, C::BM),
-                            (int)(gridDim.x / (unsigned)tiles_n));
-    if ((int)blockIdx.x >= tiles_m * tiles_n) return;
-    int tm, tn;
-    tile_order(blockIdx.x, tiles_m, tiles_n, C::GROUP_M, &tm, &tn);
-    int e, first, end;
-    if (!find_block(p.offsets, p.experts, p.rows, C::BM, tm, &e, &first, &end)) return;
+__device__ __forceinline__ void grouped_block(const GroupedProblem &p, float *lds, int e,
+                                              int first, int end, int tn) {
     // the expert's matrices from this block's first row on
     const GemmArgs g{end - first, p.N, p.K, p.A + (int64_t)first * p.lda, p.lda,
                      p.B + e * p.strideb, p.ldb, p.C + (int64_t)first * p.ldc, p.ldc,
@@ -41,6 +29,57 @@ __global__ __launch_bounds__(C::THREADS, C::OCC) void grouped_kernel(GroupedProb
     mma_tile<C>(g, lds, m0, n0, 0, (g.K + C::BK - 1) / C::BK, acc);
     const int r_first = KwReduce<C>::run(lds, acc);
     store_tile<C>(g, m0, n0, acc, 0, n_lo, r_first, KwReduce<C>::RPG);
+}
+
+// Blocks of C.  Row blocks are counted expert by expert (find_block); the launch
+// holds the most there can be, and the work-groups past those there are leave at
+// once.  The ones there are get the XCD-aware order of the plain product, over all
+// experts' row blocks: those of one expert follow each other and share its matrix.
+template <class C>
+__global__ __launch_bounds__(C::THREADS, C::OCC) void grouped_kernel(GroupedProblem p,
+                                                                    int tiles_n) {
+    __shared__ __attribute__((aligned(16))) float lds[C::LDS_FLOATS];
+    // (offsets that are no running sum can give more blocks than were launched, or a
+    // count that wrapped to a negative one)
+    const int tiles_m = min(count_blocks(p.offsets, p.experts, p.rows, AllBlocks{C::BM}),
+                            (int)(gridDim.x / (unsigned)tiles_n));
+    if ((int)blockIdx.x >= tiles_m * tiles_n) return;
+    int tm, tn, e, first, end;
+    tile_order(blockIdx.x, tiles_m, tiles_n, C::GROUP_M, &tm, &tn);
+    if (!find_block(p.offsets, p.experts, p.rows, C::BM, tm, &e, &first, &end)) return;
+    grouped_block<C>(p, lds, e, first, end, tn);
+}
+
+// The same with blocks of two sizes: the experts' full blocks of L::BM rows, and after
+// them (in the order of the launch, where they fill the CUs as the large ones end) the
+// rows that are left, in blocks of S::BM.
+template <class L, class S>
+__global__ __launch_bounds__(L::THREADS, L::OCC) void grouped_mixed_kernel(GroupedProblem p,
+                                                                          int large_n,
+                                                                          int small_n) {
+    static_assert(L::THREADS == S::THREADS && L::OCC == S::OCC, "one launch");
+    constexpr int FLOATS = L::LDS_FLOATS > S::LDS_FLOATS ? L::LDS_FLOATS : S::LDS_FLOATS;
+    __shared__ __attribute__((aligned(16))) float lds[FLOATS];
+    const FullBlocks full{L::BM};
+    const RestBlocks rest{L::BM, S::BM};
+    const int large_m = max(0, min(count_blocks(p.offsets, p.experts, p.rows, full),
+                                   (int)(gridDim.x / (unsigned)large_n)));
+    int tm, tn, e, first, end, index, id = blockIdx.x;
+    if (id < large_m * large_n) {
+        tile_order(id, large_m, large_n, L::GROUP_M, &tm, &tn);
+        if (!find_expert(p.offsets, p.experts, p.rows, full, tm, &e, &first, &end, &index)) return;
+        first += index * L::BM;
+        if (first >= 0 && first < end) grouped_block<L>(p, lds, e, first, end, tn);
+        return;
+    }
+    id -= large_m * large_n;
+    const int small_m = min(count_blocks(p.offsets, p.experts, p.rows, rest),
+                            (int)(gridDim.x / (unsigned)small_n));
+    if (id >= small_m * small_n) return;
+    tile_order(id, small_m, small_n, S::GROUP_M, &tm, &tn);
+    if (!find_expert(p.offsets, p.experts, p.rows, rest, tm, &e, &first, &end, &index)) return;
+    first += (end - first) / L::BM * L::BM + index * S::BM;
+    if (first >= 0 && first < end) grouped_block<S>(p, lds, e, first, end, tn);
 }
 
 // Few rows of each expert: bound by reading the matrices once.  A work-group forms up
@@ -230,6 +269,24 @@ hipError_t launch_blocks(const GroupedProblem &p, hipStream_t s) {
                   (int)tiles_n);
 }
 
+// Full blocks of T, the rest in blocks of U (with R register sets).
+template <class T, class U, bool TB, int R>
+hipError_t launch_mixed(const GroupedProblem &p, hipStream_t s) {
+    if (!narrow(T::BM, p.lda, T::BK) ||
+        !(TB ? narrow(T::BN, p.ldb, T::BK) : narrow(T::BK, p.ldb, T::BN)))
+        return launch_blocks<Cfg<TileSmall, false, TB, false, 1>>(p, s);
+    using L = Cfg<T, false, TB, true, 1>;
+    using S = Cfg<U, false, TB, true, R>;
+    const int64_t large_n = ((int64_t)p.N + L::BN - 1) / L::BN;
+    const int64_t small_n = ((int64_t)p.N + S::BN - 1) / S::BN;
+    const int64_t with_rows = p.rows < p.experts ? p.rows : p.experts;
+    const int64_t rest = with_rows * (L::BM / S::BM);  // at most
+    const int64_t blocks = p.rows / L::BM * large_n + rest * small_n;
+    if (blocks > most_groups(L::THREADS)) return hipErrorInvalidValue;
+    return launch(grouped_mixed_kernel<L, S>, dim3((unsigned)blocks), dim3(L::THREADS), 0, s, p,
+                  (int)large_n, (int)small_n);
+}
+
 template <bool TB>
 hipError_t launch_few(const GroupedProblem &p, hipStream_t s) {
     const int64_t row_blocks = most_blocks(p.rows, p.experts, kFewRows);
@@ -269,15 +326,22 @@ hipError_t launch_grouped_ta_tile(const GroupedTaProblem &p, hipStream_t s) {
 // The configuration by the rows an expert has on average (the host knows no more).
 // Smaller blocks waste less of the last block of each expert, larger ones read the
 // operands less often.  Times in us, B as given / transposed, the experts uneven:
-//   rows, experts, N x K      32x32        64x64     128x128   192x128
+//   rows, experts, N x K      32x32        64x64     128x128   192x128   128x128, rest 64x64
 //     48, 8, 4096 x 2048     55 / 68     73 / 78   129 / 231  193 / 362
 //    512, 64, 1024 x 512     33 / 34     42 / 40    69 / 70    99 / 98
 //    400, 8, 4096 x 2048     95 / 92    102 / 124  131 / 231  199 / 367
-//    700, 8, 4096 x 2048    149 / 151   134 / 132  230 / 232  195 / 366
-//   8192, 8, 4096 x 2048   1220 / 1192 1041 / 1069 1060 / 1146 1067 / 1071
-//  16384, 4, 4096 x 4096   4768 / 4769 4179 / 4300 3932 / 3945 3848 / 3888
-// (the first two rows against 54 and 27 us to read the matrices at 5 TB/s, the last two
-// against 893 and 3570 us at the 154 TFLOP/s of a large plain product).  32 x 32 blocks
+//    700, 8, 4096 x 2048    149 / 151   134 / 132  230 / 232  195 / 366    168 / 157
+//    600, 2, 4096 x 4096                188 / 186                          271 / 273
+//   3000, 4, 1000 x 1000                 69 /  69                           74 /  75
+//   4000, 8, 1024 x  512                 50 /  50                           44 /  45
+//   1500, 8, 4096 x 2048                244 / 236                          234 / 235
+//   8192, 64, 2048 x 1024               383 / 375                          373 / 386
+//   8192, 8, 4096 x 2048   1220 / 1192 1103 / 1096 1060 / 1146 1067 / 1071  996 / 1010
+//  16384, 4, 4096 x 4096   4768 / 4769 4179 / 4300 3932 / 3945 3848 / 3888 3770 / 3787
+//  30000, 4, 2048 x 2048                                       1779 / 1794 1783 / 1842
+// (the first two rows against 54 and 27 us to read the matrices at 5 TB/s, the last three
+// against 893, 3570 and 1634 us at the 154 TFLOP/s of a large plain product).  The blocks
+// of two sizes are taken from nearly a large one for every CU on.  32 x 32 blocks
 // with B as given have one register set for few rows on many work-groups, two else; the
 // kernel for few rows needs the many work-groups too, whether B is transposed or not:
 //   rows, experts, N x K       few rows   one set / two / transposed
@@ -292,7 +356,8 @@ hipError_t launch_grouped_ta_tile(const GroupedTaProblem &p, hipStream_t s) {
 template <bool TB>
 hipError_t launch_grouped_as(const GroupedProblem &p, hipStream_t s) {
     const int each = p.rows / p.experts;
-    if (each >= 4096) return launch_grouped_tile<TileTall, TB, 1>(p, s);
+    if (each > 128 && (double)p.rows * p.N >= 128.0 * 128 * 7 / 8 * compute_units())
+        return launch_mixed<TileWide, TileSmall, TB, 3>(p, s);
     if (each > 64) return launch_grouped_tile<TileSmall, TB, 3>(p, s);
     if (((int64_t)p.N + kFewCols - 1) / kFewCols * p.experts >= 2 * compute_units()) {
         if (each <= 8 && p.N >= 4) return launch_few<TB>(p, s);

@@ -308,6 +308,52 @@ def test_grouped_on_larger_blocks(rows, N, K, experts):
         assert np.array_equal(got[e], A[lo:hi].T.astype(np.float64) @ D[lo:hi])
 
 
+
+@pytest.mark.parametrize("groups", list(GROUPS))
+@pytest.mark.parametrize("rows,N,K,experts", [(9001, 530, 330, 2), (4100, 1000, 129, 16),
+                                              (4097, 1030, 40, 3)])
+def test_grouped_on_blocks_of_two_sizes(rows, N, K, experts, groups):
+    """Many rows of each expert: full blocks, and smaller ones for the rows past them."""
+    torch = torch_cuda()
+    rng = np.random.default_rng(rows + experts)
+    offsets = GROUPS[groups](rows, experts)
+    dev_off = torch.from_numpy(offsets.astype(np.int32)).cuda()
+    A, B, C = int_matrix(rng, rows, K), int_matrix(rng, experts, K, N), int_matrix(rng, rows, N)
+    dB = torch.from_numpy(B).cuda()
+    for trans, (alpha, beta) in itertools.product((False, True), ((1.0, 0.0), (0.5, -2.0))):
+        mat = dB.transpose(1, 2).contiguous().transpose(1, 2) if trans else dB
+        dA, _ = padded(torch, torch.from_numpy(A), 3, offset=1)
+        dA[:offsets[0]] = float("nan")  # rows of no expert
+        dA[offsets[-1]:] = float("nan")
+        dC, buf = padded(torch, torch.from_numpy(C), 1, offset=2)
+        sg.grouped_matmul(dA, mat, dev_off, out=dC, alpha=alpha, beta=beta)
+        want, _ = plain_grouped(A.astype(np.float64), B.astype(np.float64), offsets,
+                                C.astype(np.float64), alpha, beta)
+        assert np.array_equal(dC.double().cpu().numpy(), want)
+        dC[:] = SENT
+        assert int((buf != SENT).sum()) == 0, "wrote outside C"
+
+
+def test_grouped_on_blocks_of_two_sizes_follows_no_offset_out_of_its_rows():
+    torch = torch_cuda()
+    rng = np.random.default_rng(1)
+    rows, N, K, experts = 4200, 1000, 33, 8
+    A, B = int_matrix(rng, rows, K), int_matrix(rng, experts, K, N)
+    dA, dB = torch.from_numpy(A).cuda(), torch.from_numpy(B).cuda()
+    bad = [-2**31, -1, 100, 4000, 2**31 - 1, 7, 7, 7, -3]
+    dC, buf = padded(torch, torch.full((rows, N), 1.0), 3, offset=5)
+    sg.grouped_matmul(dA, dB, torch.tensor(bad, dtype=torch.int32, device="cuda"), out=dC)
+    want = np.ones((rows, N))
+    for e, lo, hi in [(1, 0, 100), (2, 100, 4000), (3, 4000, 4200)]:
+        want[lo:hi] = A[lo:hi].astype(np.float64) @ B[e]
+    assert np.array_equal(dC.double().cpu().numpy(), want)
+    # several experts claim all rows: any result, but inside C
+    bad = [0, 2**31 - 1] * (experts // 2) + [0]
+    sg.grouped_matmul(dA, dB, torch.tensor(bad, dtype=torch.int32, device="cuda"), out=dC)
+    dC[:] = SENT
+    assert int((buf != SENT).sum()) == 0, "wrote outside C"
+
+
 def test_rows_so_long_that_offsets_pass_31_bits():
     torch = torch_cuda()
     rng = np.random.default_rng(2)
