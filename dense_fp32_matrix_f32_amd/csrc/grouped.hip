@@ -353,7 +353,6 @@ hipError_t launch_grouped_ta_tile(const GroupedTaProblem &p, hipStream_t s) {
 //    700, 8, 4096 x 2048    149 / 151   134 / 132  230 / 232  195 / 366    168 / 157
 //    600, 2, 4096 x 4096                188 / 186                          271 / 273
 //   3000, 4, 1000 x 1000                 69 /  69                           74 /  75
-//   4000, 8, 1024 x  512                 50 /  50                           44 /  45
 //   1500, 8, 4096 x 2048                244 / 236                          234 / 235
 //   8192, 64, 2048 x 1024               383 / 375                          373 / 386
 //   8192, 8, 4096 x 2048   1220 / 1192 1103 / 1096 1060 / 1146 1067 / 1071  996 / 1010
@@ -361,7 +360,16 @@ hipError_t launch_grouped_ta_tile(const GroupedTaProblem &p, hipStream_t s) {
 //  30000, 4, 2048 x 2048                                       1779 / 1794 1783 / 1842
 // (the first two rows against 54 and 27 us to read the matrices at 5 TB/s, the last three
 // against 893, 3570 and 1634 us at the 154 TFLOP/s of a large plain product).  The blocks
-// of two sizes are taken from nearly a large one for every CU on.  32 x 32 blocks
+// of two sizes are taken where there is almost one large one for every CU, or the second
+// round over the CUs is half full (last column: large blocks for a CU):
+//   rows, experts, N x K        64x64      two sizes
+//   3500,  8, 1024 x  512       42 /  40    44 /  45     0.85
+//   4000,  8, 1024 x  512       50 /  50    44 /  45     0.98
+//   7521, 17,  754 x 2376      260 / 273   295 / 275     1.38
+//   3441,  9, 1795 x  910      113 / 122   113 / 115     1.57
+//   2500,  8, 4096 x 2048      370 / 375   353 / 375     2.4
+//   5400,  8, 4096 x 2048      745 / 744   700 / 708     5.3
+// 32 x 32 blocks
 // with B as given have one register set for few rows on many work-groups, two else; the
 // kernel for few rows needs the many work-groups too, whether B is transposed or not:
 //   rows, experts, N x K       few rows   one set / two / transposed
@@ -376,7 +384,9 @@ hipError_t launch_grouped_ta_tile(const GroupedTaProblem &p, hipStream_t s) {
 template <bool TB>
 hipError_t launch_grouped_as(const GroupedProblem &p, hipStream_t s) {
     const int each = p.rows / p.experts;
-    if (each > 128 && (double)p.rows * p.N >= 128.0 * 128 * 7 / 8 * compute_units())
+    // large blocks for a CU, if there were no rows past the full ones
+    const double large = p.rows / 128.0 * std::ceil(p.N / 128.0) / compute_units();
+    if (each > 128 && (large >= 1.45 || (large >= 0.93 && large <= 1.0)))
         return launch_mixed<TileWide, TileSmall, TB, 3>(p, s);
     if (each > 64) return launch_grouped_tile<TileSmall, TB, 3>(p, s);
     if (((int64_t)p.N + kFewCols - 1) / kFewCols * p.experts >= 2 * compute_units()) {
@@ -398,13 +408,19 @@ hipError_t launch_grouped(const GroupedProblem &p, hipStream_t s) {
     return p.tb ? launch_grouped_as<true>(p, s) : launch_grouped_as<false>(p, s);
 }
 
-// 128 x 128 blocks unless they leave CUs without one (8192 rows, 8 experts, 2048 x
-// 4096: 971 us against 1015 on 64 x 64 blocks, 893 at the rate of a large plain
-// product; 48 rows: 68 against 78 us, 54 to write the result at 5 TB/s; 300 rows, 8
-// experts, 512 x 512, 128 of the large blocks: 10.1 against 7.9).
+// 128 x 128 blocks where there are many for each CU, 64 x 64 else (8192 rows; the
+// experts' numbers of rows differ, and so do the times of their blocks):
+//   experts, M x N       64x64   128x128   large blocks a CU
+//    4, 1100 x 1024     171-197  225-252     1.1
+//    8, 1024 x 1024     137-139  136-154     2
+//    8, 1024 x 1280     170-172  175-199     2.5
+//    9,  910 x 1795     242-243  248-256     4.2
+//    5, 2048 x 2048       517      470       5
+//    8, 2048 x 4096      1020      980      16     (893 at the rate of a large product)
+// and with 48 rows, 8, 2048 x 4096, 78 against 68 (54 to write the result at 5 TB/s).
 hipError_t launch_grouped_ta(const GroupedTaProblem &p, hipStream_t s) {
     const double large = std::ceil(p.M / 128.0) * std::ceil(p.N / 128.0) * p.experts;
-    return large > compute_units() ? launch_grouped_ta_tile<TileWide>(p, s)
+    return large > 4.5 * compute_units() ? launch_grouped_ta_tile<TileWide>(p, s)
                                    : launch_grouped_ta_tile<TileSmall>(p, s);
 }
 
