@@ -64,7 +64,8 @@ def make_ids(rng, tokens, top, experts, dropped=0.1, skew=0):
 @pytest.mark.parametrize("tokens,top,experts", [
     (1, 1, 1), (1, 8, 64), (3, 2, 5), (63, 1, 2), (64, 1, 3), (65, 4, 64), (127, 8, 65),
     (1000, 3, 17), (1024, 1, 256), (2049, 2, 7), (5000, 8, 300), (20000, 1, 1), (33333, 3, 129),
-    (4096, 8, 1000), (70001, 2, 64), (300, 2, 5000)])
+    (4096, 8, 1000), (70001, 2, 64), (300, 2, 5000),
+    (2047, 3, 17), (2049, 3, 895), (30001, 3, 511), (30001, 3, 512), (9999, 7, 895)])
 @pytest.mark.parametrize("dropped", [0.0, 0.3])
 def test_sort(tokens, top, experts, dropped):
     log(f"[gpu] sort {tokens} x {top}, {experts} experts, dropped {dropped}")
