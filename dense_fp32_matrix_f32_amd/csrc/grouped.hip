@@ -1,6 +1,7 @@
-// grouped.hip -- the products of experts' rows, one launch for all experts, on
-// the block kernel of mfma_kernel.h: a work-group finds its expert from the
-// device's offsets and computes one block of that expert's product.
+// grouped.hip -- the products of experts' rows, one launch for all experts: a
+// work-group finds its expert from the device's offsets and computes one block of that
+// expert's product, with the block kernel of mfma_kernel.h or, for a few rows of each
+// expert, with one of its own.
 #include "experts.h"
 #include "groups.h"
 #include "mfma_kernel.h"
@@ -360,8 +361,8 @@ hipError_t launch_grouped_ta_tile(const GroupedTaProblem &p, hipStream_t s) {
 //  30000, 4, 2048 x 2048                                       1779 / 1794 1783 / 1842
 // (the first two rows against 54 and 27 us to read the matrices at 5 TB/s, the last three
 // against 893, 3570 and 1634 us at the 154 TFLOP/s of a large plain product).  The blocks
-// of two sizes are taken where there is almost one large one for every CU, or the second
-// round over the CUs is half full (last column: large blocks for a CU):
+// of two sizes are taken where there is almost one large one for every CU, or a second
+// round over the CUs is nearly half full (last column: large blocks for a CU):
 //   rows, experts, N x K        64x64      two sizes
 //   3500,  8, 1024 x  512       42 /  40    44 /  45     0.85
 //   4000,  8, 1024 x  512       50 /  50    44 /  45     0.98
