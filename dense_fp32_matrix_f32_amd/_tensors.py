@@ -66,28 +66,46 @@ def dense(t, shape, name, dtype, device):
         raise ValueError(f"{name} must be contiguous")
 
 
+def launch_stream(stream, index):
+    """`stream`, which a caller passed, as a torch stream on GPU number `index`."""
+    if isinstance(stream, torch.cuda.Stream):
+        return stream
+    if not stream.cuda_stream:  # ExternalStream would make a new one of the null handle
+        return torch.cuda.default_stream(index)
+    return torch.cuda.ExternalStream(stream.cuda_stream, device=index)
+
+
+def new(like, shape, stream, dtype=None):
+    """A tensor on like's GPU, of its type unless `dtype` is given, for a call on `stream`
+    to write.  torch's allocator hands memory freed on a stream to the next allocation for
+    that stream without waiting for the work there that still uses it.  So what a
+    stream that is passed in is to write is allocated for that stream, and marked as
+    used on the current one, where the caller reads and frees it."""
+    if stream is None:
+        return like.new_empty(shape) if dtype is None else like.new_empty(shape, dtype=dtype)
+    index = like.get_device()
+    current = torch.cuda.current_stream(index)
+    with torch.cuda.stream(launch_stream(stream, index)):
+        t = like.new_empty(shape, dtype=dtype)
+    t.record_stream(current)
+    return t
+
+
 _entries = {}   # library functions by name, looked up once
 
 
-def call(entry, index, stream, made, *args):
+def call(entry, index, stream, *args):
     """entry(*args, stream) on GPU number `index`, on `stream` (default: torch's
-    current stream there).  Tensors allocated for this call (`made`) are marked as
-    used on a stream that is passed in, so that torch's allocator does not hand
-    their memory out before the work there is done."""
+    current stream there)."""
     f = _entries.get(entry)
     if f is None:
         f = _entries[entry] = getattr(lib(), entry)
     if stream is None and index == current_device():
         # the current stream's handle without a Stream object: 0.1 instead of 1.9 us
         status = f(*args, raw_stream(index))
-    elif stream is not None:
-        with torch.cuda.device(index):
-            status = f(*args, stream.cuda_stream)
-        if isinstance(stream, torch.cuda.Stream):
-            for t in made:
-                t.record_stream(stream)
     else:
         with torch.cuda.device(index):
-            status = f(*args, raw_stream(index))
+            status = f(*args, raw_stream(index) if stream is None
+                       else launch_stream(stream, index).cuda_stream)
     if status != 0:
         raise SgemmError(status, entry)

@@ -2,9 +2,11 @@
 for torch tensors: the entry points of include/sgemm_f32_experts.h.
 
 Each call is enqueued on ``stream`` (default: torch's current stream on the
-tensors' device) without synchronising.  Float tensors are float32 with a unit
-column stride; a row stride (a view of a wider tensor) is passed as it is.  There
-is no autograd here: the gradients are functions of their own.
+tensors' device) without synchronising.  A stream that is passed in has to wait for
+the work that makes the inputs, and what reads the results for that stream, as with
+torch's own operations on a stream.  Float tensors are float32 with a unit column
+stride; a row stride (a view of a wider tensor) is passed as it is.  There is no
+autograd here: the gradients are functions of their own.
 
     routing = sort_by_expert(ids, experts)            # ids: tokens x top, int32
     rows = gather_rows(x, routing)                    # backward: combine_rows(drows, routing)
@@ -19,7 +21,7 @@ from typing import NamedTuple
 import torch
 
 from ._binding import lib
-from ._tensors import INT_MAX, MOST, call, dense, matrix, place
+from ._tensors import INT_MAX, MOST, call, dense, matrix, new, place
 
 
 class Routing(NamedTuple):
@@ -64,16 +66,12 @@ def sort_by_expert(ids, experts, stream=None):
     if tokens * top > MOST or not 0 <= experts <= MOST:
         raise ValueError(f"{tokens} x {top} pairs for {experts} experts do not fit 32-bit numbers")
     device = ids.get_device()
-    offsets = ids.new_empty(experts + 1)
-    order = ids.new_empty(tokens * top)
-    position = ids.new_empty((tokens, top))
+    offsets = new(ids, experts + 1, stream)
+    order = new(ids, tokens * top, stream)
+    position = new(ids, (tokens, top), stream)
     need = lib().sgemm_f32_route_workspace_size(tokens, top, experts)
-    made = [offsets, order, position]
-    workspace = None
-    if need:
-        workspace = ids.new_empty(need // 4)
-        made.append(workspace)
-    call("sgemm_f32_route_sort", device, stream, made, tokens, top, experts, ids.data_ptr(), ld,
+    workspace = new(ids, need // 4, stream) if need else None
+    call("sgemm_f32_route_sort", device, stream, tokens, top, experts, ids.data_ptr(), ld,
          offsets.data_ptr(), order.data_ptr(), position.data_ptr(),
          workspace.data_ptr() if need else 0, need)
     return Routing(offsets, order, position)
@@ -87,11 +85,11 @@ def gather_rows(x, routing, out=None, stream=None):
     ldx = matrix(x, tokens, None, "x", device=device)
     width = x.shape[1]
     if out is None:
-        out = x.new_empty((tokens * top, width))
-        made, ldo = (out,), width or 1
+        out = new(x, (tokens * top, width), stream)
+        ldo = width or 1
     else:
-        made, ldo = (), matrix(out, tokens * top, width, "out", device=device)
-    call("sgemm_f32_route_gather", device, stream, made, tokens, top, width,
+        ldo = matrix(out, tokens * top, width, "out", device=device)
+    call("sgemm_f32_route_gather", device, stream, tokens, top, width,
          position.data_ptr(), x.data_ptr(), ldx, out.data_ptr(), ldo)
     return out
 
@@ -105,11 +103,11 @@ def combine_rows(rows, routing, weights=None, out=None, stream=None):
     width = rows.shape[1]
     ldw = 1 if weights is None else matrix(weights, tokens, top, "weights", device=device)
     if out is None:
-        out = rows.new_empty((tokens, width))
-        made, ldo = (out,), width or 1
+        out = new(rows, (tokens, width), stream)
+        ldo = width or 1
     else:
-        made, ldo = (), matrix(out, tokens, width, "out", device=device)
-    call("sgemm_f32_route_combine", device, stream, made, tokens, top, width,
+        ldo = matrix(out, tokens, width, "out", device=device)
+    call("sgemm_f32_route_combine", device, stream, tokens, top, width,
          position.data_ptr(), 0 if weights is None else weights.data_ptr(), ldw,
          rows.data_ptr(), ldr, out.data_ptr(), ldo)
     return out
@@ -124,22 +122,19 @@ def combine_rows_grad(dout, rows, routing, weights=None, drows=None, stream=None
     ldd = matrix(dout, tokens, None, "dout", device=device)
     width = dout.shape[1]
     ldr = matrix(rows, tokens * top, width, "rows", device=device)
-    made = []
     dweights, ldw = None, 1
     if weights is not None:
         ldw = matrix(weights, tokens, top, "weights", device=device)
         if ldw == max(top, 1):
-            dweights = weights.new_empty((tokens, top))
+            dweights = new(weights, (tokens, top), stream)
         else:  # the library gives the gradient the weights' row stride
-            dweights = weights.new_empty((tokens, ldw))[:, :top]
-        made.append(dweights)
+            dweights = new(weights, (tokens, ldw), stream)[:, :top]
     if drows is None:
-        drows = rows.new_empty((tokens * top, width))
-        made.append(drows)
+        drows = new(rows, (tokens * top, width), stream)
         lddr = width or 1
     else:
         lddr = matrix(drows, tokens * top, width, "drows", device=device)
-    call("sgemm_f32_route_combine_grad", device, stream, made, tokens, top, width,
+    call("sgemm_f32_route_combine_grad", device, stream, tokens, top, width,
          position.data_ptr(), 0 if weights is None else weights.data_ptr(), ldw,
          rows.data_ptr(), ldr, dout.data_ptr(), ldd, drows.data_ptr(), lddr,
          0 if dweights is None else dweights.data_ptr())
@@ -187,11 +182,11 @@ def grouped_matmul(A, B, offsets, out=None, alpha=1.0, beta=0.0, stream=None):
     if out is None:
         if beta != 0.0:
             raise ValueError("beta != 0 needs out")
-        out = A.new_empty((rows, N))
-        made, ldc = (out,), N or 1
+        out = new(A, (rows, N), stream)
+        ldc = N or 1
     else:
-        made, ldc = (), matrix(out, rows, N, "out", device=device)
-    call("sgemm_f32_grouped", device, stream, made, int(trans), rows, N, K, experts,
+        ldc = matrix(out, rows, N, "out", device=device)
+    call("sgemm_f32_grouped", device, stream, int(trans), rows, N, K, experts,
          offsets.data_ptr(), float(alpha), A.data_ptr(), lda, B.data_ptr(), ldb, strideb,
          float(beta), out.data_ptr(), ldc)
     return out
@@ -208,19 +203,18 @@ def grouped_matmul_ta(A, D, offsets, out=None, alpha=1.0, beta=0.0, stream=None)
     ldd = matrix(D, rows, None, "D", device=device)
     N = D.shape[1]
     experts = _offsets(offsets, device)
-    made = ()
     if out is None:
         if beta != 0.0:
             raise ValueError("beta != 0 needs out")
-        out = A.new_empty((experts, M, N))
-        made, ldc, stridec = (out,), N or 1, M * N
+        out = new(A, (experts, M, N), stream)
+        ldc, stridec = N or 1, M * N
     else:
         if tuple(out.shape) != (experts, M, N):
             raise ValueError("out has the wrong shape")
         ldc, stridec, trans = _stack(out, "out", device)
         if trans:
             raise ValueError("out must hold row-major matrices")
-    call("sgemm_f32_grouped_ta", device, stream, made, rows, M, N, experts, offsets.data_ptr(),
+    call("sgemm_f32_grouped_ta", device, stream, rows, M, N, experts, offsets.data_ptr(),
          float(alpha), A.data_ptr(), lda, D.data_ptr(), ldd, float(beta), out.data_ptr(), ldc,
          stridec)
     return out

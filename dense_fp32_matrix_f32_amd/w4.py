@@ -6,14 +6,16 @@ include/sgemm_f32_w4.h.
     C = matmul_w4(A, w, offsets=offsets)   # rows by expert (a stack of matrices)
 
 Weights are laid out once; each call is enqueued on ``stream`` (default: torch's
-current stream on the tensors' device) without synchronising.
+current stream on the tensors' device) without synchronising.  A stream that is passed
+in has to wait for the work that makes the inputs, and what reads the results for that
+stream, as with torch's own operations on a stream.
 """
 from __future__ import annotations
 
 import torch
 
 from ._binding import W4_SCALE_BF16, W4_SCALE_F16, W4_SCALE_F32, lib
-from ._tensors import INT_MAX, MOST, call, dense, matrix
+from ._tensors import INT_MAX, MOST, call, dense, matrix, new
 from .experts import _offsets, _stack
 
 SCALE_TYPES = {torch.float32: W4_SCALE_F32, torch.float16: W4_SCALE_F16,
@@ -36,7 +38,7 @@ class W4Weights:
                 f"{'with' if self.zeros else 'without'} zero points)")
 
 
-def _new(experts, stacked, K, N, group, scale_dtype, zeros, device):
+def _new(experts, stacked, K, N, group, scale_dtype, zeros, like, stream):
     if scale_dtype not in SCALE_TYPES:
         raise TypeError("scales must be float32, float16 or bfloat16")
     if group not in (32, 64) and (group <= 0 or group % 128 != 0):
@@ -45,7 +47,7 @@ def _new(experts, stacked, K, N, group, scale_dtype, zeros, device):
         raise ValueError("sizes beyond 32 bits")
     kind = SCALE_TYPES[scale_dtype]
     size = lib().sgemm_f32_w4_packed_size(experts, N, K, group, kind, int(zeros))
-    packed = torch.empty(size, dtype=torch.uint8, device=device)
+    packed = new(like, size, stream, torch.uint8)
     return W4Weights(packed, experts, stacked, K, N, group, kind, bool(zeros))
 
 
@@ -68,8 +70,8 @@ def w4_pack(codes, scales, zeros=None, *, K, group, stream=None):
     dense(scales, lead + (groups, N), "scales", scales.dtype, codes.get_device())
     if zeros is not None:
         dense(zeros, lead + (groups, N), "zeros", torch.uint8, codes.get_device())
-    w = _new(experts, stacked, K, N, group, scales.dtype, zeros is not None, codes.device)
-    call("sgemm_f32_w4_pack", codes.get_device(), stream, [w.packed], experts, N, K, group,
+    w = _new(experts, stacked, K, N, group, scales.dtype, zeros is not None, codes, stream)
+    call("sgemm_f32_w4_pack", codes.get_device(), stream, experts, N, K, group,
          codes.data_ptr(), scales.data_ptr(), w.scale_type,
          0 if zeros is None else zeros.data_ptr(), w.packed.data_ptr(), w.packed.numel())
     return w
@@ -87,8 +89,8 @@ def w4_quantize(B, group=128, zeros=False, scale_dtype=torch.float32, stream=Non
     if trans:
         raise ValueError("B must hold row-major matrices")
     experts, K, N = stack.shape
-    w = _new(experts, stacked, K, N, group, scale_dtype, zeros, B.device)
-    call("sgemm_f32_w4_quantize", B.get_device(), stream, [w.packed], experts, N, K, group,
+    w = _new(experts, stacked, K, N, group, scale_dtype, zeros, B, stream)
+    call("sgemm_f32_w4_quantize", B.get_device(), stream, experts, N, K, group,
          B.data_ptr(), ldb, strideb, w.scale_type, int(w.zeros), w.packed.data_ptr(),
          w.packed.numel())
     return w
@@ -97,8 +99,8 @@ def w4_quantize(B, group=128, zeros=False, scale_dtype=torch.float32, stream=Non
 def w4_unpack(w, stream=None):
     """The float32 matrices that w stands for, [experts x] K x N."""
     device = w.packed.get_device()
-    out = torch.empty((w.experts, w.K, w.N), dtype=torch.float32, device=w.packed.device)
-    call("sgemm_f32_w4_unpack", device, stream, [out], w.experts, w.N, w.K, w.group, w.scale_type,
+    out = new(w.packed, (w.experts, w.K, w.N), stream, torch.float32)
+    call("sgemm_f32_w4_unpack", device, stream, w.experts, w.N, w.K, w.group, w.scale_type,
          int(w.zeros), w.packed.data_ptr(), w.packed.numel(), out.data_ptr(), max(w.N, 1),
          w.K * w.N)
     return out if w.stacked else out[0]
@@ -118,15 +120,15 @@ def matmul_w4(A, w, offsets=None, out=None, stream=None):
     elif _offsets(offsets, device) != w.experts:
         raise ValueError(f"{offsets.numel()} offsets for {w.experts} experts")
     if out is None:
-        out = A.new_empty((rows, w.N))
-        made, ldc = (out,), w.N or 1
+        out = new(A, (rows, w.N), stream)
+        ldc = w.N or 1
     else:
-        made, ldc = (), matrix(out, rows, w.N, "out", device=device)
+        ldc = matrix(out, rows, w.N, "out", device=device)
     if offsets is None:
-        call("sgemm_f32_w4", device, stream, made, rows, w.N, w.K, A.data_ptr(), lda,
+        call("sgemm_f32_w4", device, stream, rows, w.N, w.K, A.data_ptr(), lda,
              w.packed.data_ptr(), w.group, w.scale_type, int(w.zeros), out.data_ptr(), ldc)
     else:
-        call("sgemm_f32_w4_experts", device, stream, made, rows, w.N, w.K, w.experts,
+        call("sgemm_f32_w4_experts", device, stream, rows, w.N, w.K, w.experts,
              offsets.data_ptr(), A.data_ptr(), lda, w.packed.data_ptr(), w.group, w.scale_type,
              int(w.zeros), out.data_ptr(), ldc)
     return out

@@ -1,0 +1,113 @@
+"""Results of calls on a stream that is passed in, next to work that still runs on the
+current stream over memory of the results' size that has just been freed."""
+import numpy as np
+import pytest
+
+import dense_fp32_matrix_f32_amd as sg
+from gpu_helpers import log, torch_cuda
+
+pytestmark = pytest.mark.gpu
+
+
+def tensors(result):
+    """The tensors of a result: itself, packed weights, or a tuple of these."""
+    if isinstance(result, sg.W4Weights):
+        return [result.packed]
+    if isinstance(result, tuple):
+        return [t for r in result for t in tensors(r)]
+    return [] if result is None else [result]
+
+
+def check(call):
+    """call(stream) on a side stream, while the current stream still has to read blocks
+    that were freed there and have the sizes of the results: the call may neither
+    change what is read nor give other results."""
+    torch = torch_cuda()
+    want = [t.clone() for t in tensors(call(None))]
+    side = torch.cuda.Stream()
+    big = torch.ones((4096, 4096), device="cuda")
+    slow = torch.empty_like(big)
+    torch.cuda.synchronize()
+    for _ in range(2):
+        # three blocks for each result, and as many for a workspace
+        freed = [torch.full_like(t, 3) for t in want for _ in range(3)]
+        read = [torch.zeros_like(t) for t in freed]
+        torch.cuda.synchronize()
+        for _ in range(4):
+            torch.mm(big, big, out=slow)  # a millisecond each
+        for r, t in zip(read, freed):
+            r.copy_(t)
+        places = {t.data_ptr() for t in freed if t.numel()}
+        del freed, t
+        got = tensors(call(side))
+        mine = {t.data_ptr() for t in got if t.numel()}
+        side.synchronize()
+        torch.cuda.synchronize()
+        assert not places & mine, "memory that the current stream still reads was written"
+        for r in read:
+            assert r.eq(3).all()
+        for a, b in zip(got, want):
+            assert torch.equal(a, b)
+        del got, read
+
+
+def routed():
+    torch = torch_cuda()
+    rng = np.random.default_rng(5)
+    ids = torch.from_numpy(rng.integers(0, 8, (3000, 3)).astype(np.int32)).cuda()
+    x = torch.from_numpy(rng.integers(-4, 5, (3000, 72)).astype(np.float32)).cuda()
+    y = torch.from_numpy(rng.integers(-4, 5, (9000, 72)).astype(np.float32)).cuda()
+    w = torch.from_numpy(rng.integers(1, 4, (3000, 3)).astype(np.float32)).cuda()
+    B = torch.from_numpy(rng.integers(-4, 5, (8, 72, 72)).astype(np.float32)).cuda()
+    return sg.sort_by_expert(ids, 8), ids, x, y, w, B
+
+
+@pytest.mark.parametrize("name", ["sort", "gather", "combine", "combine_grad", "grouped",
+                                  "grouped_ta"])
+def test_rows_and_products_by_expert(name):
+    log(f"[gpu] {name} on another stream over freed memory")
+    r, ids, x, y, w, B = routed()
+    check({"sort": lambda s: sg.sort_by_expert(ids, 8, stream=s),
+           "gather": lambda s: sg.gather_rows(x, r, stream=s),
+           "combine": lambda s: sg.combine_rows(y, r, w, stream=s),
+           "combine_grad": lambda s: sg.combine_rows_grad(x, y, r, w, stream=s),
+           "grouped": lambda s: sg.grouped_matmul(y, B, r.offsets, stream=s),
+           "grouped_ta": lambda s: sg.grouped_matmul_ta(y, y, r.offsets, stream=s)}[name])
+
+
+@pytest.mark.parametrize("name", ["pack", "quantize", "unpack", "product", "by expert"])
+def test_4_bit_weights(name):
+    torch = torch_cuda()
+    log(f"[gpu] 4-bit {name} on another stream over freed memory")
+    r, _, _, y, _, _ = routed()
+    rng = np.random.default_rng(6)
+    # sizes without padding, so that every byte of the packed array is written
+    codes = torch.from_numpy(rng.integers(0, 256, (8, 64, 64)).astype(np.uint8)).cuda()
+    scales = torch.ones((8, 4, 64), device="cuda")
+    stack = sg.w4_pack(codes, scales, K=128, group=32)
+    one = sg.w4_pack(codes[0], scales[0], K=128, group=32)
+    full = sg.w4_unpack(stack)
+    a = torch.from_numpy(rng.integers(-4, 5, (9000, 128)).astype(np.float32)).cuda()
+    check({"pack": lambda s: sg.w4_pack(codes, scales, K=128, group=32, stream=s),
+           "quantize": lambda s: sg.w4_quantize(full, group=32, stream=s),
+           "unpack": lambda s: sg.w4_unpack(stack, stream=s),
+           "product": lambda s: sg.matmul_w4(a, one, stream=s),
+           "by expert": lambda s: sg.matmul_w4(a, stack, offsets=r.offsets, stream=s)}[name])
+
+
+@pytest.mark.parametrize("null", [False, True])
+def test_a_stream_known_by_its_handle(null):
+    """An object that only holds a stream's handle will do, the null stream's included."""
+    torch = torch_cuda()
+    side = torch.cuda.Stream()
+    r, ids, x, _, _, _ = routed()
+
+    class Handle:
+        cuda_stream = 0 if null else side.cuda_stream
+
+    want = sg.gather_rows(x, r)
+    torch.cuda.synchronize()
+    with torch.cuda.stream(torch.cuda.Stream()):
+        got = sg.gather_rows(x, r, stream=Handle())
+    (torch.cuda.default_stream() if null else side).synchronize()
+    assert torch.equal(got, want)
