@@ -103,29 +103,30 @@ def matmul(A, B, out=None, algo="auto", stream=None, alpha=1.0, beta=0.0, worksp
     "auto", ``workspace`` (a contiguous CUDA tensor, or "auto" to allocate the
     size sgemm_f32_workspace_size asks for through torch) lets products with few
     blocks of C split k across work-groups.  The product is enqueued on
-    ``stream`` (default: torch's current stream) without synchronising; tensors
-    allocated here (``out`` when None, the "auto" workspace) are marked as used on
-    that stream, so torch's allocator does not hand their memory out again before
-    the product has finished there."""
+    ``stream`` (default: torch's current stream) without synchronising; a stream that
+    is passed in has to wait for the work that makes the operands, and what reads the
+    result for that stream.  Tensors allocated here (``out`` when None, the "auto"
+    workspace) are allocated for that stream, so their memory is none that the
+    current stream still uses, and marked as used on the current one."""
     import torch
+    from ._tensors import launch_stream, new
     pa, lda, ta = _operand(A, "A")
     pb, ldb, tb = _operand(B, "B")
     M, K = A.shape
     K2, N = B.shape
     if K != K2:
         raise ValueError(f"inner dimensions differ: {K} vs {K2}")
-    made = []  # tensors allocated here, to be marked as used on the launch stream
     if out is None:
         if beta != 0.0:
             raise ValueError("beta != 0 needs out")
-        out = torch.empty((M, N), dtype=torch.float32, device=A.device)
-        made.append(out)
+        out = new(A, (M, N), stream)
     elif tuple(out.shape) != (M, N):
         raise ValueError("out has the wrong shape")
     pc, ldc, tc = _operand(out, "out")
     if tc and M > 1 and N > 1:
         raise ValueError("out must be row-major")
-    s = stream if stream is not None else torch.cuda.current_stream(A.device)
+    s = torch.cuda.current_stream(A.device) if stream is None else \
+        launch_stream(stream, A.get_device())
     algo_id = ALGOS[algo] if isinstance(algo, str) else int(algo)
     with torch.cuda.device(A.device):
         if workspace is not None and algo_id == ALGO_AUTO:
@@ -133,8 +134,7 @@ def matmul(A, B, out=None, algo="auto", stream=None, alpha=1.0, beta=0.0, worksp
                 if workspace != "auto":
                     raise ValueError('workspace must be a tensor, "auto" or None')
                 nbytes = sgemm_f32_workspace_size(int(ta), int(tb), M, N, K)
-                workspace = torch.empty(max(nbytes // 4, 1), dtype=torch.float32, device=A.device)
-                made.append(workspace)
+                workspace = new(A, max(nbytes // 4, 1), stream)
             if not workspace.is_cuda or not workspace.is_contiguous():
                 raise ValueError("workspace must be a contiguous CUDA tensor")
             st = sgemm_f32_ex_ws(int(ta), int(tb), M, N, K, float(alpha), pa, lda, pb, ldb,
@@ -145,7 +145,4 @@ def matmul(A, B, out=None, algo="auto", stream=None, alpha=1.0, beta=0.0, worksp
                                    float(beta), pc, ldc, s.cuda_stream, algo_id)
     if st != 0:
         raise SgemmError(st)
-    if isinstance(s, torch.cuda.Stream):
-        for t in made:
-            t.record_stream(s)
     return out

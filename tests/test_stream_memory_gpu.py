@@ -95,6 +95,18 @@ def test_4_bit_weights(name):
            "by expert": lambda s: sg.matmul_w4(a, stack, offsets=r.offsets, stream=s)}[name])
 
 
+@pytest.mark.parametrize("M,N,K,workspace", [(300, 257, 131, None), (128, 96, 30000, "auto")])
+def test_matmul(M, N, K, workspace):
+    torch = torch_cuda()
+    log(f"[gpu] matmul {M}x{N}x{K} on another stream over freed memory")
+    rng = np.random.default_rng(7)
+    a, b = (torch.from_numpy(rng.integers(-4, 5, s).astype(np.float32)).cuda()
+            for s in ((M, K), (K, N)))
+    if workspace:
+        assert sg.sgemm_f32_workspace_size(0, 0, M, N, K) > 0
+    check(lambda s: sg.matmul(a, b, workspace=workspace, stream=s))
+
+
 @pytest.mark.parametrize("null", [False, True])
 def test_a_stream_known_by_its_handle(null):
     """An object that only holds a stream's handle will do, the null stream's included."""
