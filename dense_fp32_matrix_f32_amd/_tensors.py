@@ -67,7 +67,11 @@ def dense(t, shape, name, dtype, device):
 
 
 def launch_stream(stream, index):
-    """`stream`, which a caller passed, as a torch stream on GPU number `index`."""
+    """`stream`, which a caller passed, as a torch stream; raises where it says that it is
+    not one of GPU number `index`, whose memory a kernel on it could not reach."""
+    device = getattr(stream, "device", None)
+    if device is not None and device.index != index:
+        raise ValueError(f"the stream is one of {device}, the tensors live on GPU {index}")
     if isinstance(stream, torch.cuda.Stream):
         return stream
     if not stream.cuda_stream:  # ExternalStream would make a new one of the null handle

@@ -275,3 +275,17 @@ def test_more_blocks_than_a_launch_holds_are_refused():
                                 0.0, far[3], 64, 0) == INVALID
     assert sg.sgemm_f32_w4_experts(rows, 64, 128, rows // 2, far[0], far[1], 128, far[2], 128, 0, 0,
                                    far[3], 64, 0) == INVALID
+
+
+def test_a_stream_of_another_gpu_is_refused():
+    """A kernel on it would run on that GPU, over memory of this one."""
+    torch = pytest.importorskip("torch")
+    from dense_fp32_matrix_f32_amd._tensors import launch_stream
+
+    class Stream:
+        device = torch.device("cuda", 1)
+        cuda_stream = 0x10
+
+    for index in (0, 2):
+        with pytest.raises(ValueError, match="stream"):
+            launch_stream(Stream(), index)

@@ -123,3 +123,26 @@ def test_a_stream_known_by_its_handle(null):
         got = sg.gather_rows(x, r, stream=Handle())
     (torch.cuda.default_stream() if null else side).synchronize()
     assert torch.equal(got, want)
+
+
+def test_a_stream_of_another_gpu_is_refused():
+    torch = torch_cuda()
+    r, ids, x, y, w, B = routed()
+    one = sg.w4_quantize(B[0], group=32)
+
+    class Other:
+        device = torch.device("cuda", torch.cuda.current_device() + 1)
+        cuda_stream = torch.cuda.Stream().cuda_stream
+
+    out = torch.empty_like(y)
+    for f in (lambda s: sg.sort_by_expert(ids, 8, stream=s), lambda s: sg.gather_rows(x, r, stream=s),
+              lambda s: sg.gather_rows(x, r, out=out, stream=s),
+              lambda s: sg.combine_rows(y, r, stream=s),
+              lambda s: sg.combine_rows_grad(x, y, r, w, stream=s),
+              lambda s: sg.grouped_matmul(y, B, r.offsets, out=out, stream=s),
+              lambda s: sg.grouped_matmul_ta(y, y, r.offsets, stream=s),
+              lambda s: sg.w4_quantize(B, group=32, stream=s), lambda s: sg.w4_unpack(one, stream=s),
+              lambda s: sg.matmul_w4(y, one, out=out, stream=s),
+              lambda s: sg.matmul(y, B[0], out=out, stream=s)):
+        with pytest.raises(ValueError, match="stream"):
+            f(Other())
