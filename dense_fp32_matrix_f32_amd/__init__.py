@@ -79,15 +79,17 @@ def _layout(rows, cols, s0, s1, name):
     raise ValueError(f"{name} needs a unit stride in one dimension")
 
 
-def _operand(t, name):
-    """(pointer, leading dimension, transposed) of a 2-D float32 CUDA tensor that is
-    row-major (unit column stride) or the transpose of a row-major array (unit row
-    stride, e.g. ``X.t()``)."""
+def _operand(t, name, device=None):
+    """(pointer, leading dimension, transposed) of a 2-D float32 CUDA tensor (on
+    `device`, if given) that is row-major (unit column stride) or the transpose of a
+    row-major array (unit row stride, e.g. ``X.t()``)."""
     import torch
     if not isinstance(t, torch.Tensor) or t.dtype != torch.float32 or t.dim() != 2:
         raise TypeError(f"{name} must be a 2-D float32 torch tensor")
     if t.device.type != "cuda":
         raise ValueError(f"{name} must live on the GPU")
+    if device is not None and t.device != device:
+        raise ValueError(f"{name} lives on {t.device}, A on {device}")
     rows, cols = t.shape
     ld, trans = _layout(rows, cols, t.stride(0), t.stride(1), name)
     return t.data_ptr(), ld, trans
@@ -111,7 +113,7 @@ def matmul(A, B, out=None, algo="auto", stream=None, alpha=1.0, beta=0.0, worksp
     import torch
     from ._tensors import launch_stream, new
     pa, lda, ta = _operand(A, "A")
-    pb, ldb, tb = _operand(B, "B")
+    pb, ldb, tb = _operand(B, "B", A.device)
     M, K = A.shape
     K2, N = B.shape
     if K != K2:
@@ -122,7 +124,7 @@ def matmul(A, B, out=None, algo="auto", stream=None, alpha=1.0, beta=0.0, worksp
         out = new(A, (M, N), stream)
     elif tuple(out.shape) != (M, N):
         raise ValueError("out has the wrong shape")
-    pc, ldc, tc = _operand(out, "out")
+    pc, ldc, tc = _operand(out, "out", A.device)
     if tc and M > 1 and N > 1:
         raise ValueError("out must be row-major")
     s = torch.cuda.current_stream(A.device) if stream is None else \
@@ -135,8 +137,8 @@ def matmul(A, B, out=None, algo="auto", stream=None, alpha=1.0, beta=0.0, worksp
                     raise ValueError('workspace must be a tensor, "auto" or None')
                 nbytes = sgemm_f32_workspace_size(int(ta), int(tb), M, N, K)
                 workspace = new(A, max(nbytes // 4, 1), stream)
-            if not workspace.is_cuda or not workspace.is_contiguous():
-                raise ValueError("workspace must be a contiguous CUDA tensor")
+            if workspace.device != A.device or not workspace.is_contiguous():
+                raise ValueError("workspace must be a contiguous CUDA tensor on A's GPU")
             st = sgemm_f32_ex_ws(int(ta), int(tb), M, N, K, float(alpha), pa, lda, pb, ldb,
                                  float(beta), pc, ldc, workspace.data_ptr(),
                                  workspace.numel() * workspace.element_size(), s.cuda_stream)

@@ -31,3 +31,18 @@ def test_layout_accepts(rows, cols, s0, s1, want):
 def test_layout_rejects_broadcast_and_overlap(rows, cols, s0, s1):
     with pytest.raises(ValueError):
         sg._layout(rows, cols, s0, s1, "X")
+
+
+def test_operands_on_different_gpus_are_refused():
+    """The kernel runs on A's GPU and could not reach the other's memory."""
+    torch = pytest.importorskip("torch")
+
+    def on(index):
+        class Placed(torch.Tensor):
+            device = property(lambda self: torch.device("cuda", index))
+        return torch.zeros(4, 4).as_subclass(Placed)
+
+    with pytest.raises(ValueError, match="B lives on cuda:1"):
+        sg.matmul(on(0), on(1))
+    with pytest.raises(ValueError, match="out lives on cuda:0"):
+        sg.matmul(on(1), on(1), out=on(0))
