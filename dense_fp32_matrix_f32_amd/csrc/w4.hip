@@ -154,7 +154,7 @@ struct Record {
         return at.f32 ? __builtin_bit_cast(float, scale[t]) : at.f16 ? wide : narrow;
     }
     __device__ __forceinline__ float zero_of(int t, const Lane<PARTS> &at) const {
-        return at.zeros ? (float)((zero >> (8 * t)) & 15) : 8.0f;
+        return at.zeros ? (float)((zero >> (8 * t)) & 255) : 8.0f;
     }
     __device__ __forceinline__ unsigned word(int j) const {
         return j == 0 ? codes.x : j == 1 ? codes.y : j == 2 ? codes.z : codes.w;

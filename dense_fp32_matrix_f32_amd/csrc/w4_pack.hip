@@ -54,7 +54,7 @@ __global__ __launch_bounds__(256) void pack_kernel(W4Layout l, int64_t records,
             }
             if (l.zeros)
                 rec[kW4Codes + l.parts * kW4Cols * l.scale_size + place] =
-                    in ? zeros[at] & 15 : 0;
+                    in ? zeros[at] : 0;
         }
     }
 }

@@ -54,7 +54,7 @@ def _new(experts, stacked, K, N, group, scale_dtype, zeros, like, stream):
 def w4_pack(codes, scales, zeros=None, *, K, group, stream=None):
     """W4Weights from codes (uint8, [experts x] ceil(K/2) x N, the code of an even k in
     the low four bits), scales ([experts x] ceil(K/group) x N, float32, float16 or
-    bfloat16) and zero points (uint8, as scales; None: 8).  All contiguous."""
+    bfloat16) and zero points (uint8, as scales, any byte; None: 8).  All contiguous."""
     if not isinstance(codes, torch.Tensor) or codes.dim() not in (2, 3):
         raise TypeError("codes must be a 2-D or 3-D uint8 torch tensor")
     stacked = codes.dim() == 3

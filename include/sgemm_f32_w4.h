@@ -5,7 +5,7 @@
  * A K x N matrix W is held as 4-bit codes q with a scale (and, if wanted, a zero
  * point) for each `group` consecutive values of a column:
  *     W[k][n] = s[k / group][n] * (q[k][n] - z[k / group][n]),
- * q in 0 .. 15, z = 8 where there are no zero points.  The product is
+ * q in 0 .. 15, z a byte (8 where there are no zero points).  The product is
  *     C[i][n] = sum over k of A[i][k] * W[k][n],
  * the definition of sgemm_f32.h with B = W.  A product with few rows is bound by
  * the bytes of B (the intensity formula of page "CUDA算子优化(4)：矩阵乘法",
@@ -23,8 +23,7 @@
  * (1e-40) are dropped, so values from 2^-110 (8e-34) on lose nothing.  Results are
  * bitwise reproducible for fixed arguments.  A NaN or infinite A[i][k] makes all of
  * row i NaN or infinite (NaN also where the definition has an infinity); values
- * beyond about 1e37 in magnitude can overflow.  Other rows are not affected.  A zero
- * point is taken modulo 16.
+ * beyond about 1e37 in magnitude can overflow.  Other rows are not affected.
  *
  * Groups.  `group` is 32, 64 or a multiple of 128 (any such value from K on
  * means one group for each column); the last group may be cut short by K.

@@ -498,3 +498,27 @@ def test_refusals_of_the_torch_layer():
     both = torch.zeros((8, 64), device=dev)
     with pytest.raises(sg.SgemmError):
         sg.matmul_w4(both[:4], w, out=both[2:6, :16])
+
+
+@pytest.mark.parametrize("rows,N,K,group", [
+    (1, 40, 3, 32), (1, 70, 300, 128), (5, 33, 129, 32), (9, 20, 200, 64), (16, 50, 260, 256),
+    (40, 64, 300, 32), (70, 130, 140, 64), (1001, 2047, 140, 32), (2100, 2000, 200, 64),
+    (513, 2900, 260, 128)])
+def test_zero_points_above_15(rows, N, K, group):
+    """Formats that keep a zero point of 16 (or any byte): taken as it is, in every kernel."""
+    torch = torch_cuda()
+    log(f"[gpu] w4 {rows} x {N} x {K} group {group}, zero points up to 255")
+    rng = np.random.default_rng(rows + K)
+    groups = -(-K // group)
+    q = rng.integers(0, 16, (K + K % 2, N)).astype(np.uint8)
+    x = rng.integers(-4, 5, (rows, K)).astype(np.float32)
+    for z in (np.full((groups, N), 16, np.uint8), rng.integers(0, 256, (groups, N)).astype(np.uint8)):
+        # |sum| <= 300 * 4 * 255 in steps of 1/2, at most 2^20 of them: exact in any order
+        s = 2.0 ** rng.integers(-1, 1, (groups, N))
+        w = sg.w4_pack(torch.from_numpy(q[0::2] | (q[1::2] << 4)).cuda(),
+                       torch.from_numpy(s).to(torch.float16).cuda(), torch.from_numpy(z).cuda(),
+                       K=K, group=group)
+        W = np.repeat(s, group, 0)[:K] * (q[:K] - np.repeat(z, group, 0)[:K].astype(np.float64))
+        assert np.array_equal(sg.w4_unpack(w).double().cpu().numpy(), W)
+        got = sg.matmul_w4(torch.from_numpy(x).cuda(), w).double().cpu().numpy()
+        assert np.array_equal(got, x.astype(np.float64) @ W)
