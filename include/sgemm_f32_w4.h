@@ -21,9 +21,15 @@
  * (q + z) rather than to |q - z|, and results are as accurate as fp32 products of
  * such terms.  The inputs enter without rounding, but bits of A[i][k] below 2^-133
  * (1e-40) are dropped, so values from 2^-110 (8e-34) on lose nothing.  Results are
- * bitwise reproducible for fixed arguments.  A NaN or infinite A[i][k] makes all of
- * row i NaN or infinite (NaN also where the definition has an infinity); values
- * beyond about 1e37 in magnitude can overflow.  Other rows are not affected.
+ * bitwise reproducible for fixed arguments.
+ *
+ * Large values.  The sums over a group, or over 128 of its k at a time, are formed
+ * before s meets them.  Nothing overflows as long as the result, and s times such a
+ * sum, have room and |A[i][k]| is at most 2.2e37 / min(group, 128): 1.7e35 for groups
+ * of 128 and more, 3.4e35 for 64 and 6.8e35 for 32 (1.3e36 / min(group, 128) with zero
+ * points above 15).  Beyond that an element can become infinite or NaN.  A NaN or
+ * infinite A[i][k] makes all of row i NaN or infinite (NaN also where the definition
+ * has an infinity).  Other rows are not affected.
  *
  * Groups.  `group` is 32, 64 or a multiple of 128 (any such value from K on
  * means one group for each column); the last group may be cut short by K.
