@@ -30,7 +30,7 @@ typedef float f32x4_any __attribute__((ext_vector_type(4), aligned(4)));
 // a launch.
 constexpr int kSortThreads = 1024, kSortWaves = kSortThreads / 64;
 constexpr int kSortChunks = 128;         // at most
-constexpr int kSortBuckets = 896;        // experts + 1 at most (63 KB of LDS)
+constexpr int kSortBuckets = 896;        // at most (63 KB of LDS)
 
 // Work-items that add up the counts of one bucket.
 __host__ __device__ constexpr int sort_slices(int buckets) { return kSortThreads / buckets; }
@@ -42,12 +42,27 @@ struct SortArgs {
     int64_t ldids;
     int run;     // pairs of a wave (a multiple of 64)
     int chunks;
-    int *counts;  // chunks x (experts + 1), or NULL with one chunk
+    int *counts;  // chunks x buckets, or NULL with one chunk
+    int buckets;  // experts + 1, or of a digit
+    // sorting by digits only:
+    const int *from;  // the pairs in the order of the digits below, or NULL: by number
+    int below;        // what the digits below count to
 };
 
-__device__ __forceinline__ int bucket_of(const SortArgs &a, int f) {
+__device__ __forceinline__ int expert_of(const SortArgs &a, int f) {
     const int e = a.ids[(int64_t)(f / a.p.top) * a.ldids + f % a.p.top];
     return e < 0 || e >= a.experts ? a.experts : e;
+}
+
+// The i-th pair and its bucket.
+template <bool DIGITS>
+__device__ __forceinline__ int pair_at(const SortArgs &a, int i) {
+    return DIGITS && a.from != nullptr ? a.from[i] : i;
+}
+template <bool DIGITS>
+__device__ __forceinline__ int bucket_of(const SortArgs &a, int f) {
+    const int e = expert_of(a, f);
+    return DIGITS ? e / a.below % a.buckets : e;
 }
 
 // The pairs of this wave (none, where its run starts past the last pair).
@@ -62,27 +77,33 @@ struct Run {
 };
 
 // The run's pairs by bucket, added to `mine`.
+template <bool DIGITS>
 __device__ __forceinline__ void count_run(const SortArgs &a, const Run &run, int *mine) {
     for (int64_t f = run.begin + (threadIdx.x & 63); f < run.end; f += 64)
-        atomicAdd(&mine[bucket_of(a, (int)f)], 1);  // sums of ones: any order gives the same
+        // sums of ones: any order gives the same
+        atomicAdd(&mine[bucket_of<DIGITS>(a, pair_at<DIGITS>(a, (int)f))], 1);
 }
 
+template <bool DIGITS>
 __global__ __launch_bounds__(kSortThreads) void sort_count_kernel(SortArgs a) {
     __shared__ int hist[kSortBuckets];
-    const int buckets = a.experts + 1;
+    const int buckets = a.buckets;
     for (int e = threadIdx.x; e < buckets; e += kSortThreads) hist[e] = 0;
     __syncthreads();
-    count_run(a, Run(a), hist);
+    count_run<DIGITS>(a, Run(a), hist);
     __syncthreads();
     for (int e = threadIdx.x; e < buckets; e += kSortThreads)
         a.counts[(int64_t)blockIdx.x * buckets + e] = hist[e];
 }
 
+// offsets and position are written where they are not NULL; without position, order gets the
+// dropped pairs too.
+template <bool DIGITS>
 __global__ __launch_bounds__(kSortThreads) void sort_place_kernel(SortArgs a, int *offsets,
                                                                   int *order, int *position) {
     extern __shared__ int next[];  // [wave][bucket]: the place of the next pair
     __shared__ int sums[kSortWaves];
-    const int buckets = a.experts + 1;
+    const int buckets = a.buckets;
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
     // the chunks' counts of a bucket, before this chunk and all, added by `slices`
     // work-items, each over every slices-th chunk
@@ -110,7 +131,7 @@ __global__ __launch_bounds__(kSortThreads) void sort_place_kernel(SortArgs a, in
     __syncthreads();
     const Run run(a);
     int *mine = next + wave * buckets;
-    count_run(a, run, mine);
+    count_run<DIGITS>(a, run, mine);
     __syncthreads();
 
     // one work-item for each bucket (kSortBuckets <= kSortThreads)
@@ -131,7 +152,7 @@ __global__ __launch_bounds__(kSortThreads) void sort_place_kernel(SortArgs a, in
     for (int w = 0; w < wave; ++w) upto += sums[w];
     if (tid < buckets) {
         const int first = upto - all;
-        if (blockIdx.x == 0) offsets[tid] = first;
+        if (!DIGITS && blockIdx.x == 0) offsets[tid] = first;
         int at = first + before;
         for (int w = 0; w < kSortWaves; ++w) {
             const int c = next[w * buckets + tid];
@@ -142,9 +163,9 @@ __global__ __launch_bounds__(kSortThreads) void sort_place_kernel(SortArgs a, in
     __syncthreads();
 
     for (int64_t base = run.begin; base < run.end; base += 64) {
-        const int f = (int)(base + lane);  // used where it is a pair
         const bool have = base + lane < run.end;
-        const int e = have ? bucket_of(a, f) : buckets;
+        const int f = have ? pair_at<DIGITS>(a, (int)(base + lane)) : 0;
+        const int e = have ? bucket_of<DIGITS>(a, f) : buckets;
         // the lanes with the same bucket
         unsigned long long same = __ballot(have);
         for (int bit = 1; bit < buckets; bit *= 2) {
@@ -154,8 +175,13 @@ __global__ __launch_bounds__(kSortThreads) void sort_place_kernel(SortArgs a, in
         if (have) {
             const unsigned long long below = same & ((1ull << lane) - 1);
             const int at = mine[e] + __popcll(below);
-            position[f] = e < a.experts ? at : -1;
-            order[at] = e < a.experts ? f : -1;
+            if (DIGITS && position == nullptr) {
+                order[at] = f;
+            } else {
+                const bool kept = (DIGITS ? expert_of(a, f) : e) < a.experts;
+                position[f] = kept ? at : -1;
+                order[at] = kept ? f : -1;
+            }
         }
         // the last lane of each bucket moves its place on, after all have read it
         __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
@@ -166,42 +192,77 @@ __global__ __launch_bounds__(kSortThreads) void sort_place_kernel(SortArgs a, in
     }
 }
 
-// More experts than fit LDS: one work-group for a bucket.  It counts the pairs of the
-// buckets below its own, then walks all pairs in order and gives its own the places
-// from there on, ranked by a ballot in a wave and a running sum over waves.
+// More experts than fit LDS: the same stable sort by one digit of the expert's number
+// after the other, the lowest first.  The digits have the smallest base that makes do
+// with as few of them as possible.  What remains is where each expert's pairs begin,
+// which a search of the order for its number gives.
+struct Digits {
+    int count, base;
+
+    explicit Digits(int experts) : count(1), base(kSortBuckets) {
+        const int64_t numbers = (int64_t)experts + 1;  // dropped pairs have the last
+        while (power(base) < numbers) ++count;
+        while (power(base - 1) >= numbers) --base;
+    }
+    int64_t power(int x) const {
+        int64_t r = 1;
+        for (int i = 0; i < count; ++i) r *= x;
+        return r;
+    }
+};
+
+__global__ __launch_bounds__(256) void sort_offsets_kernel(SortArgs a, const int *order,
+                                                           int *offsets) {
+    const int n = a.p.count();
+    for (int64_t e = (int64_t)blockIdx.x * 256 + threadIdx.x; e <= a.experts;
+         e += (int64_t)gridDim.x * 256) {
+        int lo = 0, hi = n;  // the first place of an expert not below e
+        while (lo < hi) {
+            const int mid = lo + (hi - lo) / 2, f = order[mid];
+            if ((f < 0 ? a.experts : expert_of(a, f)) < e)
+                lo = mid + 1;
+            else
+                hi = mid;
+        }
+        offsets[e] = lo;
+    }
+}
+
+// Few pairs for not many more experts than fit LDS, in one launch: one work-group for a
+// bucket.  It counts the pairs of the buckets below its own, then walks all pairs in
+// order and gives its own the places from there on, ranked by a ballot in a wave and a
+// running sum over waves.
 __global__ __launch_bounds__(kSortThreads) void sort_each_kernel(SortArgs a, int *offsets,
                                                                  int *order, int *position) {
     __shared__ int sums[kSortWaves];
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-    const int n = a.p.count();
-    for (int64_t me = blockIdx.x; me <= a.experts; me += gridDim.x) {
-        int below = 0;
-        for (int64_t f = tid; f < n; f += kSortThreads) below += bucket_of(a, (int)f) < me;
-        for (int d = 32; d; d /= 2) below += __shfl_xor(below, d);
-        if (lane == 0) sums[wave] = below;
+    const int n = a.p.count(), me = blockIdx.x;
+    int below = 0;
+    for (int f = tid; f < n; f += kSortThreads) below += expert_of(a, f) < me;
+    for (int d = 32; d; d /= 2) below += __shfl_xor(below, d);
+    if (lane == 0) sums[wave] = below;
+    __syncthreads();
+    int place = 0;
+    for (int w = 0; w < kSortWaves; ++w) place += sums[w];
+    if (tid == 0) offsets[me] = place;
+    __syncthreads();
+    for (int base = 0; base < n; base += kSortThreads) {
+        const int f = base + tid;
+        const bool mine = f < n && expert_of(a, f) == me;
+        const unsigned long long who = __ballot(mine);
+        if (lane == 0) sums[wave] = __popcll(who);
         __syncthreads();
-        int place = 0;
-        for (int w = 0; w < kSortWaves; ++w) place += sums[w];
-        if (tid == 0) offsets[me] = place;
-        __syncthreads();
-        for (int64_t base = 0; base < n; base += kSortThreads) {
-            const int64_t f = base + tid;
-            const bool mine = f < n && bucket_of(a, (int)f) == me;
-            const unsigned long long who = __ballot(mine);
-            if (lane == 0) sums[wave] = __popcll(who);
-            __syncthreads();
-            int at = place;
-            for (int w = 0; w < kSortWaves; ++w) {
-                if (w < wave) at += sums[w];
-                place += sums[w];
-            }
-            if (mine) {
-                at += __popcll(who & ((1ull << lane) - 1));
-                position[f] = me < a.experts ? at : -1;
-                order[at] = me < a.experts ? (int)f : -1;
-            }
-            __syncthreads();
+        int at = place;
+        for (int w = 0; w < kSortWaves; ++w) {
+            if (w < wave) at += sums[w];
+            place += sums[w];
         }
+        if (mine) {
+            at += __popcll(who & ((1ull << lane) - 1));
+            position[f] = me < a.experts ? at : -1;
+            order[at] = me < a.experts ? f : -1;
+        }
+        __syncthreads();
     }
 }
 
@@ -215,6 +276,24 @@ void sort_cut(int64_t n, int *run, int *chunks) {
     *run = (int)((chunk + kSortThreads - 1) / kSortThreads * 64);
     const int64_t per = (int64_t)*run * kSortWaves;
     *chunks = n > 0 ? (int)((n + per - 1) / per) : 1;
+}
+
+// Whether a work-group for each bucket takes the call instead of the digits.  Times of a
+// call / of its kernels in us:
+//   pairs, experts       each bucket     digits
+//      8,    896          10 /   6      17 /   9
+//   6144,    896          21 /  21      36 /  36
+//   6144,   1536          32 /  32      37 /  37
+//   4096,   2048          29 /  29      29 /  28
+//   1024,   3000          17 /  17      18 /  15
+//   2048,   3000          24 /  24      20 /  20
+//      8,   4096          17 /  17      17 /  10
+//   1024,   4096          23 /  22      17 /  15
+//   8192,   1024          30 /  30      27 /  25
+// and 262144 pairs for 1024 experts 830 against 38 (22 for 895 experts in one pass),
+// 2^20 pairs for 2^20 experts 178 in three digits.
+bool sort_each(int64_t n, int chunks, int experts) {
+    return chunks == 1 && experts * (n + 4096) <= 1 << 24;
 }
 
 // ---------------------------------------------------------------------------
@@ -460,28 +539,59 @@ int span_for(int64_t groups, int width, int lanes) {
 size_t route_workspace(Pairs p, int experts) {
     int run, chunks;
     sort_cut(p.count(), &run, &chunks);
-    return experts < kSortBuckets && chunks > 1 ? sizeof(int) * chunks * (size_t)(experts + 1) : 0;
+    if (experts < kSortBuckets)
+        return chunks > 1 ? sizeof(int) * chunks * (size_t)(experts + 1) : 0;
+    if (sort_each(p.count(), chunks, experts)) return 0;
+    // the counts, and the pairs between two digits
+    const size_t counts = chunks > 1 ? (size_t)chunks * Digits(experts).base : 0;
+    return sizeof(int) * (counts + (size_t)p.count());
 }
 
-hipError_t launch_route_sort(Pairs p, int experts, const int *ids, int64_t ldids, int *offsets,
-                             int *order, int *position, void *workspace, hipStream_t s) {
-    SortArgs a{p, experts, ids, ldids, 0, 0, (int *)workspace};
-    sort_cut(p.count(), &a.run, &a.chunks);
-    if (experts >= kSortBuckets)
-        return launch(sort_each_kernel, dim3(route_groups((int64_t)experts + 1)),
-                      dim3(kSortThreads), 0, s, a, offsets, order, position);
-    const int buckets = experts + 1;
-    size_t lds = sizeof(int) * kSortWaves * (size_t)buckets;
+namespace {
+
+// One pass of the sort.
+template <bool DIGITS>
+hipError_t launch_sort_pass(SortArgs a, int *offsets, int *order, int *position, hipStream_t s) {
+    size_t lds = sizeof(int) * kSortWaves * (size_t)a.buckets;
     if (a.chunks == 1) {
         a.counts = nullptr;
     } else {
-        lds += 2 * sizeof(int) * sort_slices(buckets) * (size_t)buckets;
-        const hipError_t e = launch(sort_count_kernel, dim3((unsigned)a.chunks),
+        lds += 2 * sizeof(int) * sort_slices(a.buckets) * (size_t)a.buckets;
+        const hipError_t e = launch(sort_count_kernel<DIGITS>, dim3((unsigned)a.chunks),
                                     dim3(kSortThreads), 0, s, a);
         if (e != hipSuccess) return e;
     }
-    return launch(sort_place_kernel, dim3((unsigned)a.chunks), dim3(kSortThreads), lds, s, a,
-                  offsets, order, position);
+    return launch(sort_place_kernel<DIGITS>, dim3((unsigned)a.chunks), dim3(kSortThreads), lds, s,
+                  a, offsets, order, position);
+}
+
+}  // namespace
+
+hipError_t launch_route_sort(Pairs p, int experts, const int *ids, int64_t ldids, int *offsets,
+                             int *order, int *position, void *workspace, hipStream_t s) {
+    SortArgs a{p, experts, ids, ldids, 0, 0, (int *)workspace, experts + 1, nullptr, 1};
+    sort_cut(p.count(), &a.run, &a.chunks);
+    if (experts < kSortBuckets) return launch_sort_pass<false>(a, offsets, order, position, s);
+    if (sort_each(p.count(), a.chunks, experts))
+        return launch(sort_each_kernel, dim3((unsigned)experts + 1), dim3(kSortThreads), 0, s, a,
+                      offsets, order, position);
+    if (p.count() > 0) {
+        const Digits digits(experts);
+        a.buckets = digits.base;
+        int *between = a.counts + (a.chunks > 1 ? (size_t)a.chunks * digits.base : 0);
+        for (int left = digits.count - 1; left >= 0; --left) {
+            // the last pass but one ends in `between`, the one before it in `order`
+            int *to = left % 2 == 0 ? order : between;
+            const hipError_t e = launch_sort_pass<true>(a, nullptr, to,
+                                                        left == 0 ? position : nullptr, s);
+            if (e != hipSuccess) return e;
+            a.from = to;
+            if (left > 0) a.below *= digits.base;
+        }
+    }
+    const int64_t groups = ((int64_t)experts + 256) / 256;
+    return launch(sort_offsets_kernel, dim3(route_groups(groups)), dim3(256), 0, s, a, order,
+                  offsets);
 }
 
 hipError_t launch_route_gather(Pairs p, int width, const int *position, const float *x,

@@ -63,6 +63,9 @@ extern "C" {
  * sgemm_f32_route_workspace_size() bytes, which may be 0 (then it may be NULL);
  * calls that overlap in time must not share it.  The size is 0 for invalid
  * arguments too.
+ * The pairs are walked twice for up to 895 experts, and twice for each digit of the
+ * experts' numbers beyond (two digits up to 802815 experts, at most four), but for
+ * a few thousand pairs of a few thousand experts, which one launch sorts.
  */
 size_t sgemm_f32_route_workspace_size(int tokens, int top, int experts);
 hipError_t sgemm_f32_route_sort(int tokens, int top, int experts,

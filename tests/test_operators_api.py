@@ -289,3 +289,28 @@ def test_a_stream_of_another_gpu_is_refused():
     for index in (0, 2):
         with pytest.raises(ValueError, match="stream"):
             launch_stream(Stream(), index)
+
+
+@pytest.mark.parametrize("experts", [896, 897, 5000, 802815, 802816, 719323135, 719323136,
+                                     2**31 - 65537])
+def test_digits_of_the_sort_for_many_experts(experts):
+    """From 896 experts on the pairs are sorted by digits: the workspace holds the counts of
+    a digit for each of the chunks, and the pairs between two digits."""
+    tokens, top = 1 << 20, 8
+    pairs = tokens * top
+    need = sg.sgemm_f32_route_workspace_size(tokens, top, experts)
+    base, rest = divmod(need // 4 - pairs, 128)
+    assert rest == 0 and 2 <= base <= 896
+    digits = next(d for d in range(1, 9) if 896**d > experts)
+    assert base**digits > experts and (base - 1)**digits <= experts
+    # one chunk, by digits or with a work-group for each expert
+    assert sg.sgemm_f32_route_workspace_size(100, 8, experts) == (3200 if experts >= 5000 else 0)
+    assert sg.sgemm_f32_route_workspace_size(0, 8, experts) == 0
+    if experts < 5000:
+        return
+    big = {**SORT, "tokens": 100, "top": 8, "ldids": 8, "experts": experts, "ws_bytes": 3200}
+    offsets_end = B + 4 * (experts + 1)
+    assert offsets_end <= C
+    for bad in [dict(ws=0), dict(ws_bytes=3199), dict(ws=E + 4), dict(ws=A + 16), dict(ws=C + 16),
+                dict(ws=offsets_end // 16 * 16 - 16)]:
+        _refused("sgemm_f32_route_sort", big, bad, SORT)
