@@ -1,5 +1,12 @@
-// w4_pack.hip -- 4-bit weights into the layout of w4.h and back.  These run once
-// for a set of weights; each is one pass bound by memory traffic.
+// w4_pack.hip -- 4-bit weights into the layout of w4.h and back.  These run once for a
+// set of weights and are simple rather than fast; none reaches the rate of a copy (5.0
+// TB/s).  With f16 scales, in us, the bytes counted once:
+//   matrices, group             pack             quantize         unpack
+//    1 of 4096 x 4096,   32     10 (1.8 TB/s)      41 (1.9)        70 (1.1)
+//    1 of 4096 x 4096,  128     10 (1.8)           91 (0.8)        70 (1.1)
+//    1 of 4096 x 4096, 4096     10 (1.7)         2480 (0.03)       72 (1.1)
+//   64 of 2048 x 2048,  128    124 (2.2)          731 (1.7)       890 (1.4)
+//    8 of 8192 x 8192,  128    357 (1.6)         1437 (1.7)      1758 (1.4)
 #include "w4.h"
 
 namespace sgemm {
@@ -59,7 +66,8 @@ __global__ __launch_bounds__(256) void pack_kernel(W4Layout l, int64_t records,
     }
 }
 
-// One work-item for each group of a column: its extremes, then its codes.
+// One work-item for each group of a column: its extremes, then its codes, so B is read
+// twice, and groups of many k leave few work-items, each waiting for its loads.
 __global__ __launch_bounds__(256) void quantize_kernel(W4Layout l, int64_t items, int groups,
                                                        const float *__restrict__ B, int64_t ldb,
                                                        int64_t strideb,
@@ -114,6 +122,7 @@ __global__ __launch_bounds__(256) void quantize_kernel(W4Layout l, int64_t items
     }
 }
 
+// One work-item for each element.
 __global__ __launch_bounds__(256) void unpack_kernel(W4Layout l, int64_t items,
                                                      const unsigned char *__restrict__ packed,
                                                      float *__restrict__ B, int64_t ldb,
