@@ -146,3 +146,37 @@ def test_a_stream_of_another_gpu_is_refused():
               lambda s: sg.matmul(y, B[0], out=out, stream=s)):
         with pytest.raises(ValueError, match="stream"):
             f(Other())
+
+
+def test_another_stream_inside_a_capture():
+    """Calls on a stream that a capture has forked to: replayed on new inputs, with eager
+    work between the replays."""
+    torch = torch_cuda()
+    r, ids, x, _, w, B = routed()
+    side, out = torch.cuda.Stream(), torch.empty_like(x)
+
+    def layer(stream):
+        r = sg.sort_by_expert(ids, 8, stream=stream)
+        h = sg.grouped_matmul(sg.gather_rows(x, r, stream=stream), B, r.offsets, stream=stream)
+        return sg.combine_rows(h, r, w, stream=stream), sg.matmul(x, B[0], stream=stream)
+
+    layer(side)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        side.wait_stream(torch.cuda.current_stream())
+        got = layer(side)
+        torch.cuda.current_stream().wait_stream(side)
+        out.copy_(got[0])
+    for seed in range(3):
+        g = torch.Generator(device="cuda").manual_seed(seed)
+        ids.copy_(torch.randint(-1, 8, ids.shape, generator=g, device="cuda"))
+        x.copy_(torch.randint(-4, 5, x.shape, generator=g, device="cuda"))
+        want = layer(None)
+        torch.cuda.synchronize()
+        for t in got:
+            t.fill_(float("nan"))
+        graph.replay()
+        torch.cuda.synchronize()
+        for a, b in zip((*got, out), (*want, want[0])):
+            assert torch.equal(a, b)
