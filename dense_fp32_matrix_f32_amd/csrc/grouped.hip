@@ -361,8 +361,9 @@ hipError_t launch_grouped_ta_tile(const GroupedTaProblem &p, hipStream_t s) {
 //  30000, 4, 2048 x 2048                                       1779 / 1794 1783 / 1842
 // (the first two rows against 54 and 27 us to read the matrices at 5 TB/s, the last three
 // against 893, 3570 and 1634 us at the 154 TFLOP/s of a large plain product).  The blocks
-// of two sizes are taken where there is almost one large one for every CU, or a second
-// round over the CUs is nearly half full (last column: large blocks for a CU):
+// of two sizes are taken where there is almost one large one for every CU (0.93 to 1.0,
+// measured at 0.85 and 0.98), or a second round over the CUs is nearly half full (last
+// column: large blocks for a CU):
 //   rows, experts, N x K        64x64      two sizes
 //   3500,  8, 1024 x  512       42 /  40    44 /  45     0.85
 //   4000,  8, 1024 x  512       50 /  50    44 /  45     0.98

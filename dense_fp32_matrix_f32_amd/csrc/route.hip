@@ -418,6 +418,8 @@ __global__ __launch_bounds__(256) void gather_kernel(Pairs p, int width, int lan
 //   16384 tokens of 2048, four choices                       597   589
 //   32768 tokens of 2048, eight choices                     2370  2251
 //   4096 tokens of 2048, four choices (134 MB)               146   165
+// (with new buffers the bound helps at 268 MB; buffers that stay, and sizes a little past
+// it, lose 6 to 8%, larger ones and wider rows gain again)
 bool store_past(Pairs p, int width) {
     return (int64_t)p.count() * width * 4 >= (int64_t)256 << 20;
 }

@@ -722,11 +722,14 @@ hipError_t launch_many_rows(const W4Layout &l, const W4Problem &p, hipStream_t s
 //   rows  N x K, group      choice           others
 //   1     4096 x 4096, 128  one strip 4.5    two 5.3; 4 waves 5.3, 16 waves 4.6
 //   1     8192 x 8192, 128  one strip 9.5    two 9.4; 4 waves 10.2, 16 waves 9.5
-//   8 by expert, 64 x 2048 x 2048, 128: two strips 6.8, one 8.1
+//   8 by expert, 64 x 2048 x 2048, 128: two strips 6.8, one 8.1 (1024 work-groups; between
+//                           512 and that neither was measured)
 //   5     4096 x 4096, 64   5-row form 5.5   10-row form 6.9
 //   8     4096 x 4096, 128  10-row form 6.8  16-row form 7.9
 //   16    4096 x 4096, 128  one strip 9.7    two 10.2, four 13.0; 10-row form 9.7
 //   16    8192 x 8192, 64   two strips 19.1  one 32.8, four 24.6
+//   16    5120 to 7168 x 8192, 64  one strip 33 (12 rows 28): more work-groups than CUs, but
+//                           not the 512 from which two strips are taken; two not measured
 //   32    4096 x 4096, 128  two strips 10.6  one 17.2, four 13.5
 //   256 by expert, 16 x 1408 x 4096, 32: many rows 42, two strips 44, one 64, four 49
 //   256 by expert, 16 x 2048 x 2048, 128: many rows 19, two strips 26

@@ -6,7 +6,8 @@ tensors' device) without synchronising.  A stream that is passed in has to wait 
 the work that makes the inputs, and what reads the results for that stream, as with
 torch's own operations on a stream.  Float tensors are float32 with a unit column
 stride; a row stride (a view of a wider tensor) is passed as it is.  There is no
-autograd here: the gradients are functions of their own.
+autograd here: a result takes no part in a graph, also where an input requires a
+gradient; the gradients are functions of their own.
 
     routing = sort_by_expert(ids, experts)            # ids: tokens x top, int32
     rows = gather_rows(x, routing)                    # backward: combine_rows(drows, routing)

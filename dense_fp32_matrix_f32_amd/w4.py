@@ -8,7 +8,9 @@ include/sgemm_f32_w4.h.
 Weights are laid out once; each call is enqueued on ``stream`` (default: torch's
 current stream on the tensors' device) without synchronising.  A stream that is passed
 in has to wait for the work that makes the inputs, and what reads the results for that
-stream, as with torch's own operations on a stream.
+stream, as with torch's own operations on a stream.  There is no autograd here: a
+result takes no part in a graph, also where an input requires a gradient, and the
+product has no gradient of its own (w4_unpack() gives the matrices for one).
 """
 from __future__ import annotations
 
