@@ -88,9 +88,20 @@ def new(like, shape, stream, dtype=None):
     if stream is None:
         return like.new_empty(shape) if dtype is None else like.new_empty(shape, dtype=dtype)
     index = like.get_device()
+    stream = launch_stream(stream, index)
+    if stream.cuda_stream == raw_stream(index):
+        return like.new_empty(shape, dtype=dtype)
     current = torch.cuda.current_stream(index)
-    with torch.cuda.stream(launch_stream(stream, index)):
-        t = like.new_empty(shape, dtype=dtype)
+    if index == current_device():
+        # as torch.cuda.stream() does, without its context: 6.4 instead of 9.9 us
+        torch.cuda.set_stream(stream)
+        try:
+            t = like.new_empty(shape, dtype=dtype)
+        finally:
+            torch.cuda.set_stream(current)
+    else:
+        with torch.cuda.stream(stream):
+            t = like.new_empty(shape, dtype=dtype)
     t.record_stream(current)
     return t
 
@@ -104,12 +115,12 @@ def call(entry, index, stream, *args):
     f = _entries.get(entry)
     if f is None:
         f = _entries[entry] = getattr(lib(), entry)
-    if stream is None and index == current_device():
-        # the current stream's handle without a Stream object: 0.1 instead of 1.9 us
-        status = f(*args, raw_stream(index))
+    # the current stream's handle without a Stream object: 0.1 instead of 1.9 us
+    handle = raw_stream(index) if stream is None else launch_stream(stream, index).cuda_stream
+    if index == current_device():
+        status = f(*args, handle)
     else:
         with torch.cuda.device(index):
-            status = f(*args, raw_stream(index) if stream is None
-                       else launch_stream(stream, index).cuda_stream)
+            status = f(*args, handle)
     if status != 0:
         raise SgemmError(status, entry)

@@ -67,11 +67,10 @@ def sort_by_expert(ids, experts, stream=None):
     if tokens * top > MOST or not 0 <= experts <= MOST:
         raise ValueError(f"{tokens} x {top} pairs for {experts} experts do not fit 32-bit numbers")
     device = ids.get_device()
-    offsets = new(ids, experts + 1, stream)
-    order = new(ids, tokens * top, stream)
-    position = new(ids, (tokens, top), stream)
+    empty = ids.new_empty if stream is None else lambda shape: new(ids, shape, stream)
+    offsets, order, position = empty(experts + 1), empty(tokens * top), empty((tokens, top))
     need = lib().sgemm_f32_route_workspace_size(tokens, top, experts)
-    workspace = new(ids, need // 4, stream) if need else None
+    workspace = empty(need // 4) if need else None
     call("sgemm_f32_route_sort", device, stream, tokens, top, experts, ids.data_ptr(), ld,
          offsets.data_ptr(), order.data_ptr(), position.data_ptr(),
          workspace.data_ptr() if need else 0, need)
