@@ -54,7 +54,7 @@ __device__ __forceinline__ int expert_of(const SortArgs &a, int f) {
     return e < 0 || e >= a.experts ? a.experts : e;
 }
 
-// The i-th pair and its bucket.
+// The pair that is the i-th to be sorted, and a pair's bucket.
 template <bool DIGITS>
 __device__ __forceinline__ int pair_at(const SortArgs &a, int i) {
     return DIGITS && a.from != nullptr ? a.from[i] : i;
@@ -96,8 +96,8 @@ __global__ __launch_bounds__(kSortThreads) void sort_count_kernel(SortArgs a) {
         a.counts[(int64_t)blockIdx.x * buckets + e] = hist[e];
 }
 
-// offsets and position are written where they are not NULL; without position, order gets the
-// dropped pairs too.
+// By digits, offsets are not written, and without position (all digits but the last) order
+// gets the dropped pairs too.
 template <bool DIGITS>
 __global__ __launch_bounds__(kSortThreads) void sort_place_kernel(SortArgs a, int *offsets,
                                                                   int *order, int *position) {
