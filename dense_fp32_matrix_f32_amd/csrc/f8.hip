@@ -147,7 +147,9 @@ __device__ __forceinline__ void f8_tile(const F8Args &p, unsigned char *stage0,
 
     // Copies: unit u of this wave is 8 rows of x or of w, 1024 bytes side by side in LDS; then
     // the words of scales, 64 rows a copy.  They go through buffer resources that end with the
-    // rows there are, so a block at the edge reads nothing past them.
+    // rows there are, so a block at the edge reads nothing past them.  A copy's whole place is its
+    // vector offset: the range check is sure to count that one, the scalar one it leaves out or
+    // takes from the size, which wraps where there are fewer rows than it steps over.
     const int64_t x_plane = p.x.rows * kF8Block, w_plane = p.w.rows * kF8Block;
     const unsigned char *xb = p.x.codes + block0 * x_plane + (int64_t)first * kF8Block;
     const unsigned char *wb = p.w.codes + expert * p.expert +
@@ -162,25 +164,25 @@ __device__ __forceinline__ void f8_tile(const F8Args &p, unsigned char *stage0,
         for (int u = 0; u < T::UNITS; ++u) {
             const int unit = wave + u * T::WAVES;
             const LdsBytes to = (LdsBytes)(stage + unit * 1024);
+            const int at = unit * 1024 + lane * 16;
             if (unit * 8 < T::BM)
-                __builtin_amdgcn_raw_ptr_buffer_load_lds(xr, to, 16, lane * 16, unit * 1024, 0, 0);
+                __builtin_amdgcn_raw_ptr_buffer_load_lds(xr, to, 16, at, 0, 0, 0);
             else
-                __builtin_amdgcn_raw_ptr_buffer_load_lds(wr, to, 16, lane * 16,
-                                                         unit * 1024 - T::BM * kF8Block, 0, 0);
+                __builtin_amdgcn_raw_ptr_buffer_load_lds(wr, to, 16, at - T::BM * kF8Block, 0, 0, 0);
         }
         const int word = (block0 + b) >> 2;
         if (wave < T::BM / 64) {
             const auto r = resource(p.x.scales + ((int64_t)word * p.x.rows + first) * 4, rows * 4);
             __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (LdsBytes)(stage + T::CODES + wave * 256), 4,
-                                                     lane * 4, wave * 256, 0, 0);
+                                                     wave * 256 + lane * 4, 0, 0, 0);
         }
         if constexpr (WS == W_ROWS) {
             if (wave < T::BN / 64) {
                 const auto r =
                     resource(p.w.scales + ((int64_t)word * p.w.rows + n0) * 4, w_rows * 4);
                 __builtin_amdgcn_raw_ptr_buffer_load_lds(
-                    r, (LdsBytes)(stage + T::CODES + T::BM * 4 + wave * 256), 4, lane * 4,
-                    wave * 256, 0, 0);
+                    r, (LdsBytes)(stage + T::CODES + T::BM * 4 + wave * 256), 4,
+                    wave * 256 + lane * 4, 0, 0, 0);
             }
         }
         xb += x_plane;
