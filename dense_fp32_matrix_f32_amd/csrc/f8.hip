@@ -2,18 +2,14 @@
 //
 //     C[m][n] = sum over blocks b of sx[b][m] * sw[b][n] * sum over k in b of x[m][k] * w[n][k]
 //
-// (layout and scales in f8.h).  The 8-bit matrix instructions of gfx950 form 128 products of an
-// element at three times the rate of the bf16 ones (3.8 against 1.1 PFLOP/s without loads),
-// but add each eight of them with about 14 bits below the largest: results are 1.5e-5
-// to 4e-5 off in the 2-norm on random data.  A bf16 result is rounded by 4e-3 anyway and
-// takes them.  An fp32 result does not: its codes become bf16 numbers, which hold every code
-// and power of two exactly, and the bf16 instructions add their products in fp32 (5e-8).
-// The powers of two go into the codes' conversion, or into the 8-bit instruction.  A general
-// fp32 scale of the weights meets a block's fp32 sums as they are added to the total.
-// With the 8-bit instruction its power of two goes in as well, and the total is
-// kept in units of its fraction: it is multiplied by the quotient of two blocks' fractions
-// between them, and the instruction adds to it in place, which saves the registers of the
-// block's sums (4096 x 8192 x 4096: sixteen waves of 64 x 64 then fit, 155 -> 141 us; 117 with powers of two).
+// (layout and scales in f8.h).  Sums are kept in fp32.  The 8-bit matrix instructions of gfx950 do
+// not: they form 128 products of an element at three times the rate of the bf16 ones (3.8 against
+// 1.1 PFLOP/s without loads), but add each eight of them with about 14 bits below the largest,
+// so results are 1.5e-5 to 4e-5 off in the 2-norm on random data and have no right digit where
+// large terms cancel.  The codes become bf16 numbers instead, which hold every code and power
+// of two exactly, and the bf16 instructions add their products in fp32 (5e-8).  The powers of two
+// go into the codes' conversion.  A general fp32 scale of the weights meets a block's fp32 sums as
+// they are added to the total.
 //
 // The weights are the first operand of the matrix instructions, so a lane holds four
 // neighbouring columns of a row of C.
@@ -30,7 +26,6 @@ typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
-typedef int i32x8 __attribute__((ext_vector_type(8)));
 
 // How the scales of the first operand (the weights) are kept.
 enum { W_F32, W_POW2, W_ROWS };
@@ -79,7 +74,6 @@ __device__ __forceinline__ bf16x8 to_bf16(unsigned lo, unsigned hi, float s) {
 // A lane's 32 codes of a row and block: chunks g and g + 4, g = lane / 16.
 union Codes {
     uint4 half[2];
-    i32x8 all;
     unsigned word[8];
     __device__ __forceinline__ void load(const unsigned char *p, unsigned at) {
         half[0] = *(const uint4 *)(p + at);
@@ -108,7 +102,8 @@ __device__ __forceinline__ void store4(const F8Args &p, float *C, f32x4 v, int64
     }
 }
 __device__ __forceinline__ void store4(const F8Args &p, __bf16 *C, f32x4 v, int64_t at, int left) {
-    const bf16x4 r = {(__bf16)v[0], (__bf16)v[1], (__bf16)v[2], (__bf16)v[3]};
+    // (as a vector: taken apart, the totals of 256 x 256 no longer fit the registers)
+    const bf16x4 r = __builtin_convertvector(v, bf16x4);
     if (p.wide && left >= 4) {
         *(bf16x4 *)(C + at) = r;
     } else {
@@ -129,14 +124,14 @@ struct F8Tile {
     static constexpr int THREADS = 64 * WAVES, CODES = (BM + BN) * kF8Block;
     static constexpr int STAGE = CODES + (BM + BN) * 4;  // with a word of scales a row
     static constexpr int UNITS = (BM + BN) / 8 / WAVES;  // copies of 8 rows x 128 bytes a wave makes
-    static_assert((BM + BN) % (8 * WAVES) == 0 && BM % 64 == 0 && BN % 64 == 0 &&
-                      BM / 64 <= WAVES && BN / 64 <= WAVES,
+    static constexpr int X_UNITS = BM / 8 / WAVES;  // of them of x, then those of w
+    static_assert(BM == BN && BM % (8 * WAVES) == 0 && BM % 64 == 0 && BM / 64 <= WAVES,
                   "whole copies");
 };
 
 typedef unsigned char __attribute__((address_space(3))) *LdsBytes;
 
-template <class T, bool FP32, int WS, int WT, int XT>
+template <class T, class OUT, int WS, int WT, int XT>
 __device__ __forceinline__ void f8_tile(const F8Args &p, unsigned char *stage0,
                                         unsigned char *stage1, int expert, int first, int rows,
                                         int n0, int block0, int blocks, int64_t c0) {
@@ -164,11 +159,11 @@ __device__ __forceinline__ void f8_tile(const F8Args &p, unsigned char *stage0,
         for (int u = 0; u < T::UNITS; ++u) {
             const int unit = wave + u * T::WAVES;
             const LdsBytes to = (LdsBytes)(stage + unit * 1024);
-            const int at = unit * 1024 + lane * 16;
-            if (unit * 8 < T::BM)
+            const int at = (wave + u % T::X_UNITS * T::WAVES) * 1024 + lane * 16;
+            if (u < T::X_UNITS)
                 __builtin_amdgcn_raw_ptr_buffer_load_lds(xr, to, 16, at, 0, 0, 0);
             else
-                __builtin_amdgcn_raw_ptr_buffer_load_lds(wr, to, 16, at - T::BM * kF8Block, 0, 0, 0);
+                __builtin_amdgcn_raw_ptr_buffer_load_lds(wr, to, 16, at, 0, 0, 0);
         }
         const int word = (block0 + b) >> 2;
         if (wave < T::BM / 64) {
@@ -196,23 +191,6 @@ __device__ __forceinline__ void f8_tile(const F8Args &p, unsigned char *stage0,
     const float *w_scale = (const float *)(p.w.scales + expert * p.expert) +
                            min((n0 + wn * 16 * TN) / kF8Block, (int)p.scale_cols - 1);
     float sw = 1.0f, sw_next = 1.0f;  // the scale of a block, loaded a block ahead
-    // fp32 scales with the 8-bit instruction: the biased exponent of the block's, the fraction
-    // that the totals are in units of, and what they are multiplied by before the block.  A
-    // zero (or a number below 2^-126) enters as 2^-127, the rows' scales with it, and where all
-    // are zero the unit is; infinities and NaN enter as NaN.
-    int exponent = 127, rows_scale = 255;
-    float unit = 0.0f, ratio = 1.0f;
-    auto next_unit = [&] {
-        const unsigned bits = __builtin_amdgcn_readfirstlane(__builtin_bit_cast(unsigned, sw));
-        exponent = bits >> 23 & 255;
-        rows_scale = min(exponent, 1) * 255;
-        ratio = 1.0f;
-        if (exponent != 0 && exponent != 255) {
-            const float fraction = __builtin_bit_cast(float, (bits & 0x807FFFFFu) | 0x3F800000u);
-            if (unit != 0.0f && unit != fraction) ratio = unit / fraction;
-            unit = fraction;
-        }
-    };
 
     f32x4 acc[TM][TN];
 #pragma unroll
@@ -223,65 +201,40 @@ __device__ __forceinline__ void f8_tile(const F8Args &p, unsigned char *stage0,
     auto multiply = [&](const unsigned char *s, int b) {
         const unsigned char *xs = s + T::CODES + xrow * 4 + ((block0 + b) & 3);
         const unsigned char *ws = s + T::CODES + (T::BM + wrow) * 4 + ((block0 + b) & 3);
-        if constexpr (FP32) {
-            bf16x8 w[TN][4];
+        bf16x8 w[TN][4];
 #pragma unroll
-            for (int tn = 0; tn < TN; ++tn) {
-                Codes c;
-                c.load(s, w_at + tn * 16 * kF8Block);
-                c.widen<WT>(WS == W_ROWS   ? f8_exp2(ws[64 * tn])
-                            : WS == W_POW2 ? sw
-                                           : 1.0f,
-                            w[tn]);
-            }
+        for (int tn = 0; tn < TN; ++tn) {
+            Codes c;
+            c.load(s, w_at + tn * 16 * kF8Block);
+            c.widen<WT>(WS == W_ROWS   ? f8_exp2(ws[64 * tn])
+                        : WS == W_POW2 ? sw
+                                       : 1.0f,
+                        w[tn]);
+        }
 #pragma unroll
-            for (int tm = 0; tm < TM; ++tm) {
-                Codes c;
-                c.load(s, x_at + tm * 16 * kF8Block);
-                bf16x8 x[4];
-                c.widen<XT>(f8_exp2(xs[64 * tm]), x);
-                f32x4 part[TN];
+        for (int tm = 0; tm < TM; ++tm) {
+            Codes c;
+            c.load(s, x_at + tm * 16 * kF8Block);
+            bf16x8 x[4];
+            c.widen<XT>(f8_exp2(xs[64 * tm]), x);
+            f32x4 part[TN];
 #pragma unroll
-                for (int j = 0; j < 4; ++j)
-#pragma unroll
-                    for (int tn = 0; tn < TN; ++tn) {
-                        if constexpr (WS == W_F32)
-                            part[tn] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
-                                w[tn][j], x[j], j == 0 ? f32x4{} : part[tn], 0, 0, 0);
-                        else
-                            acc[tm][tn] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
-                                w[tn][j], x[j], acc[tm][tn], 0, 0, 0);
-                    }
-                if constexpr (WS == W_F32) {
-#pragma unroll
-                    for (int tn = 0; tn < TN; ++tn)
-#pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            acc[tm][tn][e] = fmaf(sw, part[tn][e], acc[tm][tn][e]);
-                }
-            }
-        } else {
-            Codes w[TN];
-#pragma unroll
-            for (int tn = 0; tn < TN; ++tn) w[tn].load(s, w_at + tn * 16 * kF8Block);
-#pragma unroll
-            for (int tm = 0; tm < TM; ++tm) {
-                Codes x;
-                x.load(s, x_at + tm * 16 * kF8Block);
-                // with a scale of zero 2^-127 times 2^-127: no code reaches a number
-                const int sx = WS == W_F32 ? xs[64 * tm] & rows_scale : xs[64 * tm];
+            for (int j = 0; j < 4; ++j)
 #pragma unroll
                 for (int tn = 0; tn < TN; ++tn) {
-                    const int by = WS == W_POW2 ? (int)(__builtin_bit_cast(unsigned, sw) >> 23)
-                                   : WS == W_ROWS ? (int)ws[64 * tn]
-                                                  : exponent;
-                    if constexpr (WS == W_F32) {
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) acc[tm][tn][e] *= ratio;
-                    }
-                    acc[tm][tn] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
-                        w[tn].all, x.all, acc[tm][tn], WT, XT, 0, by, 0, sx);
+                    if constexpr (WS == W_F32)
+                        part[tn] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+                            w[tn][j], x[j], j == 0 ? f32x4{} : part[tn], 0, 0, 0);
+                    else
+                        acc[tm][tn] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+                            w[tn][j], x[j], acc[tm][tn], 0, 0, 0);
                 }
+            if constexpr (WS == W_F32) {
+#pragma unroll
+                for (int tn = 0; tn < TN; ++tn)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        acc[tm][tn][e] = fmaf(sw, part[tn][e], acc[tm][tn][e]);
             }
         }
     };
@@ -293,7 +246,6 @@ __device__ __forceinline__ void f8_tile(const F8Args &p, unsigned char *stage0,
         __builtin_amdgcn_s_waitcnt(0x0F70);  // vmcnt(0)
         __syncthreads();
         sw = sw_next;
-        if constexpr (!FP32 && WS == W_F32) next_unit();
         if (b + 1 < blocks) {
             copy(next, b + 1);
             if constexpr (WS != W_ROWS) sw_next = w_scale[(b + 1) * p.scale_cols];
@@ -310,7 +262,6 @@ __device__ __forceinline__ void f8_tile(const F8Args &p, unsigned char *stage0,
     }
 
     // a lane holds row i and columns 4g .. 4g+3 of each tile
-    using Out = typename std::conditional<FP32, float, __bf16>::type;
 #pragma unroll
     for (int tm = 0; tm < TM; ++tm) {
         const int m = xrow + 16 * tm;
@@ -318,15 +269,14 @@ __device__ __forceinline__ void f8_tile(const F8Args &p, unsigned char *stage0,
 #pragma unroll
         for (int tn = 0; tn < TN; ++tn) {
             const int n = n0 + wn * 16 * TN + 16 * tn + 4 * g;
-            if constexpr (!FP32 && WS == W_F32) acc[tm][tn] *= unit;
             if (n < p.N)
-                store4(p, (Out *)p.C, acc[tm][tn], c0 + (int64_t)(first + m) * p.ldc + n, p.N - n);
+                store4(p, (OUT *)p.C, acc[tm][tn], c0 + (int64_t)(first + m) * p.ldc + n, p.N - n);
         }
     }
 }
 
 // C rows = x rows times the weights of their expert.
-template <class T, bool FP32, int WS, int XT>
+template <class T, class OUT, int WS, int XT>
 __global__ __launch_bounds__(T::THREADS) void f8_kernel(F8Args p, int tiles_n) {
     __shared__ __attribute__((aligned(16))) unsigned char stage0[T::STAGE];
     __shared__ __attribute__((aligned(16))) unsigned char stage1[T::STAGE];
@@ -343,7 +293,7 @@ __global__ __launch_bounds__(T::THREADS) void f8_kernel(F8Args p, int tiles_n) {
         tile_order(blockIdx.x, gridDim.x / (unsigned)tiles_n, tiles_n, 4, &tm, &tn);
         first = tm * T::BM;
     }
-    f8_tile<T, FP32, WS, F8_E4M3, XT>(p, stage0, stage1, expert, first, min(T::BM, end - first),
+    f8_tile<T, OUT, WS, F8_E4M3, XT>(p, stage0, stage1, expert, first, min(T::BM, end - first),
                                       tn * T::BN, 0, p.blocks, 0);
 }
 
@@ -368,7 +318,7 @@ __global__ __launch_bounds__(T::THREADS) void f8_ta_kernel(F8Args p, int rows, i
     int tm, tn;
     tile_order(blockIdx.x % tiles, tiles_m, tiles_n, 4, &tm, &tn);
     const int first = tm * T::BM;
-    f8_tile<T, true, W_ROWS, WT, XT>(p, stage0, stage1, 0, first, min(T::BM, p.M - first),
+    f8_tile<T, float, W_ROWS, WT, XT>(p, stage0, stage1, 0, first, min(T::BM, p.M - first),
                                      tn * T::BN, block0, blocks, e * p.stridec);
 }
 
@@ -595,27 +545,25 @@ hipError_t launch_few_as(const F8Problem &p, const FewArgs &f, hipStream_t s) {
     return launch(f8_few_kernel<IN, RT, CT, D, false, XT, OUT>, grid, block, lds, s, f, (int)rb);
 }
 
-template <class T, bool FP32, int WS, int XT>
+template <class T, class OUT, int WS, int XT>
 hipError_t launch_many_with(const F8Problem &p, const F8Args &a, hipStream_t s) {
     const int64_t tiles_n = ((int64_t)p.N + T::BN - 1) / T::BN;
     const int64_t groups = row_blocks(p, T::BM) * tiles_n;
     if (groups > most_groups(T::THREADS)) return hipErrorInvalidValue;
     if (p.check) return hipSuccess;
-    return launch(f8_kernel<T, FP32, WS, XT>, dim3((unsigned)groups), dim3(T::THREADS), 0, s, a,
+    return launch(f8_kernel<T, OUT, WS, XT>, dim3((unsigned)groups), dim3(T::THREADS), 0, s, a,
                   (int)tiles_n);
 }
 
-template <class T, bool FP32, int XT>
+template <class T, int XT, class OUT>
 hipError_t launch_many_as(const F8Problem &p, const F8Args &a, hipStream_t s) {
-    return p.scale_type == F8_SCALE_E8M0 ? launch_many_with<T, FP32, W_POW2, XT>(p, a, s)
-                                         : launch_many_with<T, FP32, W_F32, XT>(p, a, s);
+    return p.scale_type == F8_SCALE_E8M0 ? launch_many_with<T, OUT, W_POW2, XT>(p, a, s)
+                                         : launch_many_with<T, OUT, W_F32, XT>(p, a, s);
 }
 
 using Tile64 = F8Tile<2, 2, 2, 2>;    // 64 x 64, four waves
 using Tile128 = F8Tile<2, 2, 4, 4>;   // 128 x 128, four waves
-using Tile128W = F8Tile<2, 4, 4, 2>;  // 128 x 128, eight waves
 using Tile256 = F8Tile<2, 4, 8, 4>;   // 256 x 256, eight waves
-using Tile256W = F8Tile<4, 4, 4, 4>;  // 256 x 256, sixteen waves
 
 // Rows that an expert has on average.
 int64_t rows_each(int rows, int experts, bool by_expert) {
@@ -623,42 +571,34 @@ int64_t rows_each(int rows, int experts, bool by_expert) {
 }
 
 // Tiles of C for many rows: the larger ones read each operand less often from LDS and memory,
-// the smaller ones fill the CUs with fewer rows and waste less of an expert's last one.  Times
-// in us with fp32 / power of two scales (256 x 256: eight waves for fp32 results, sixteen for bf16):
+// the smaller ones fill the CUs with fewer rows and waste less of an expert's last one.  Both
+// types of results are summed alike and differ in their stores only.  Times in us with fp32 / power
+// of two scales:
 //   rows  N x K, result             64 x 64    128 x 128   256 x 256
-//    512  4096 x 4096, fp32          29 / 24     42 / 38    108 / 91
-//   1024  4096 x 4096, fp32          46 / 41     45 / 42    108 / 91
-//   4096  8192 x 4096, fp32         325 / 281   257 / 230   222 / 196
-//   8192  8192 x 8192, fp32        1245 / 1094  963 / 838   854 / 763
-//   2048 by expert, 8 x 4096 x 2048, fp32    51 / 46     55 / 48     63 / 54
-//  16384 by expert, 8 x 2048 x 4096, fp32   338 / 292   276 / 246   330 / 281
-//  16384 by expert, 8 x 4096 x 2048, fp32   361 / 325   308 / 265   304 / 262
-//    512  4096 x 4096, bf16          24 / 19     27 / 23     57 / 50
-//   1024  8192 x 4096, bf16          67 / 52     42 / 37     59 / 53
-//   4096  8192 x 4096, bf16         238 / 211   158 / 138   139 / 115
-//   8192  8192 x 8192, bf16         899 / 770   584 / 502   483 / 413
-//   2048 by expert, 32 x 2048 x 1024, bf16   19 / 19     16 / 16     22 / 18
-//  16384 by expert, 8 x 4096 x 2048, bf16   254 / 243   190 / 182   193 / 168
-template <int XT, bool FP32>
+//    512  4096 x 4096, fp32          25 / 23     38 / 37    104 / 85
+//   1024  4096 x 4096, fp32          47 / 40     46 / 42    107 / 88
+//   4096  8192 x 4096, fp32         327 / 273   243 / 223   221 / 194
+//   8192  8192 x 8192, fp32        1197 / 1064  920 / 841   857 / 732
+//   2048 by expert, 8 x 4096 x 2048, fp32    49 / 45     51 / 48     62 / 53
+//  16384 by expert, 8 x 2048 x 4096, fp32   338 / 295   273 / 248   327 / 273
+//  16384 by expert, 8 x 4096 x 2048, fp32   363 / 322   280 / 252   302 / 265
+//    512  4096 x 4096, bf16          28 / 23     45 / 37    107 / 89
+//   1024  8192 x 4096, bf16          88 / 73     79 / 64    111 / 92
+//   4096  8192 x 4096, bf16         312 / 272   259 / 218   217 / 193
+//   8192  8192 x 8192, bf16        1200 / 1051  977 / 832   823 / 724
+//   2048 by expert, 32 x 2048 x 1024, bf16   22 / 19     24 / 21     34 / 29
+//  16384 by expert, 8 x 4096 x 2048, bf16   346 / 311   292 / 252   295 / 258
+template <int XT, class OUT>
 hipError_t launch_many(const F8Problem &p, const F8Args &a, hipStream_t s) {
     const bool by_expert = p.offsets != nullptr;
     const int64_t each = rows_each(p.rows, p.experts, by_expert), cus = compute_units();
     auto tiles = [&](int64_t b) {
         return ((int64_t)p.N + b - 1) / b * ((each + b - 1) / b) * (by_expert ? p.experts : 1);
     };
-    if (tiles(256) >= (by_expert && FP32 ? 4 : 2) * cus) {
-        if constexpr (FP32)
-            return launch_many_as<Tile256, FP32, XT>(p, a, s);
-        else
-            return launch_many_as<Tile256W, FP32, XT>(p, a, s);
-    }
-    if (tiles(128) >= cus && (!by_expert || !FP32 || each >= 512)) {
-        if constexpr (FP32)
-            return launch_many_as<Tile128, FP32, XT>(p, a, s);
-        else
-            return launch_many_as<Tile128W, FP32, XT>(p, a, s);
-    }
-    return launch_many_as<Tile64, FP32, XT>(p, a, s);
+    if (tiles(256) >= (by_expert ? 4 : 2) * cus) return launch_many_as<Tile256, XT, OUT>(p, a, s);
+    if (tiles(128) >= cus && (!by_expert || each >= 512))
+        return launch_many_as<Tile128, XT, OUT>(p, a, s);
+    return launch_many_as<Tile64, XT, OUT>(p, a, s);
 }
 
 // The kernel for codes, by the rows that share a reading of the weights.  Times in us, back
@@ -690,7 +630,7 @@ hipError_t launch_codes(const F8Problem &p, const FewArgs &f, hipStream_t s) {
         if (groups >= 512) return launch_few_as<void, 2, 2, 1, XT, OUT>(p, f, s);
         return launch_few_as<void, 2, 1, 1, XT, OUT>(p, f, s);
     }
-    return launch_many<XT, std::is_same<OUT, float>::value>(p, f.a, s);
+    return launch_many<XT, OUT>(p, f.a, s);
 }
 
 // Whether rows given as numbers are put into 8 bits by a kernel of its own.

@@ -176,8 +176,9 @@ def matmul_f8(A, w, offsets=None, out=None, out_dtype=torch.float32, dtype=torch
     """A @ W for rows A (rows x K, float32 or bfloat16, put into codes of ``dtype``; or
     F8Rows) and one 8-bit matrix, or with ``offsets`` (int32, experts + 1 values) row i
     times the matrix of its expert e, offsets[e] <= i < offsets[e+1].  The result is
-    float32 or bfloat16 (``out_dtype``, or the type of ``out``).  Rows of no expert are
-    left as they are in ``out`` (and hold anything in a result allocated here)."""
+    float32 or bfloat16 (``out_dtype``, or the type of ``out``), summed in float32 either
+    way.  Rows of no expert are left as they are in ``out`` (and hold anything in a result
+    allocated here)."""
     device = _weights(w)
     if isinstance(A, F8Rows):
         if A.K != w.K:
