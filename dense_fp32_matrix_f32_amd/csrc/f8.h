@@ -68,6 +68,20 @@ __device__ __forceinline__ int f8_scale_byte(float most, int type) {
 __device__ __forceinline__ float f8_exp2(int biased) {
     return __builtin_bit_cast(float, biased << 23);
 }
+// An fp32 scale as the power of two that goes into the codes' conversion and the rest of it, 1 to 2
+// in size, that meets the fp32 sums of a block: these are then no larger than what they add to the
+// result (sums of bare codes, up to 448 times the rows, overflowed from rows of 6e33 on).  Below
+// 2^-126 the power is 2^-127 and the rest smaller, down to zero; infinities and NaN are the rest.
+struct F8Scale {
+    float power, rest;
+};
+__device__ __forceinline__ F8Scale f8_split(float s) {
+    const unsigned bits = __builtin_bit_cast(unsigned, s), e = bits >> 23 & 255;
+    const float one = __builtin_bit_cast(float, (bits & 0x807FFFFFu) | 0x3F800000u);
+    const float power = __builtin_bit_cast(
+        float, e == 0 ? 0x00400000u : e == 255 ? 0x3F800000u : bits & 0x7F800000u);
+    return {power, e == 0 ? s * f8_exp2(254) : e == 255 ? s : one};
+}
 // 2^(127 - byte), byte in 3 .. 247
 __device__ __forceinline__ float f8_inverse(int byte) { return f8_exp2(254 - byte); }
 

@@ -8,8 +8,8 @@
 // so results are 1.5e-5 to 4e-5 off in the 2-norm on random data and have no right digit where
 // large terms cancel.  The codes become bf16 numbers instead, which hold every code and power
 // of two exactly, and the bf16 instructions add their products in fp32 (5e-8).  The powers of two
-// go into the codes' conversion.  A general fp32 scale of the weights meets a block's fp32 sums as
-// they are added to the total.
+// go into the codes' conversion.  So does that of a general fp32 scale of the weights, and the rest
+// of it meets a block's fp32 sums as they are added to the total (f8_split()).
 //
 // The weights are the first operand of the matrix instructions, so a lane holds four
 // neighbouring columns of a row of C.
@@ -201,15 +201,17 @@ __device__ __forceinline__ void f8_tile(const F8Args &p, unsigned char *stage0,
     auto multiply = [&](const unsigned char *s, int b) {
         const unsigned char *xs = s + T::CODES + xrow * 4 + ((block0 + b) & 3);
         const unsigned char *ws = s + T::CODES + (T::BM + wrow) * 4 + ((block0 + b) & 3);
+        // (taken apart here: next to its load it would wait for the copies that were asked for before)
+        const F8Scale scale =
+            WS == W_F32 ? f8_split(__builtin_bit_cast(
+                              float, __builtin_amdgcn_readfirstlane(__builtin_bit_cast(int, sw))))
+                        : F8Scale{sw, 1.0f};
         bf16x8 w[TN][4];
 #pragma unroll
         for (int tn = 0; tn < TN; ++tn) {
             Codes c;
             c.load(s, w_at + tn * 16 * kF8Block);
-            c.widen<WT>(WS == W_ROWS   ? f8_exp2(ws[64 * tn])
-                        : WS == W_POW2 ? sw
-                                       : 1.0f,
-                        w[tn]);
+            c.widen<WT>(WS == W_ROWS ? f8_exp2(ws[64 * tn]) : scale.power, w[tn]);
         }
 #pragma unroll
         for (int tm = 0; tm < TM; ++tm) {
@@ -234,7 +236,7 @@ __device__ __forceinline__ void f8_tile(const F8Args &p, unsigned char *stage0,
                 for (int tn = 0; tn < TN; ++tn)
 #pragma unroll
                     for (int e = 0; e < 4; ++e)
-                        acc[tm][tn][e] = fmaf(sw, part[tn][e], acc[tm][tn][e]);
+                        acc[tm][tn][e] = fmaf(scale.rest, part[tn][e], acc[tm][tn][e]);
             }
         }
     };
@@ -431,7 +433,8 @@ __global__ __launch_bounds__(64 * kFewWaves) void f8_few_kernel(FewArgs f, int r
             codes.half[0] = b.w[c][0];
             codes.half[1] = b.w[c][1];
             bf16x8 w[4];
-            codes.widen<F8_E4M3>(POW2 ? b.s[c] : 1.0f, w);
+            const F8Scale scale = POW2 ? F8Scale{b.s[c], 1.0f} : f8_split(b.s[c]);
+            codes.widen<F8_E4M3>(scale.power, w);
 #pragma unroll
             for (int r = 0; r < RT; ++r) {
                 f32x4 sum = POW2 ? total[r][c] : f32x4{};
@@ -443,7 +446,7 @@ __global__ __launch_bounds__(64 * kFewWaves) void f8_few_kernel(FewArgs f, int r
                 } else {
 #pragma unroll
                     for (int e = 0; e < 4; ++e)
-                        total[r][c][e] = fmaf(b.s[c], sum[e], total[r][c][e]);
+                        total[r][c][e] = fmaf(scale.rest, sum[e], total[r][c][e]);
                 }
             }
         }

@@ -26,18 +26,20 @@
  *
  * Arithmetic.  Products of codes and powers of two are exact and are added in fp32, for
  * results of either type; a bf16 result is rounded once from that (to nearest, ties to
- * even).  fp32 scales of the weights multiply a block's sum before it is added.  Results
- * are bitwise reproducible for fixed arguments.
+ * even).  Of an fp32 scale of the weights what is not a power of two multiplies a block's
+ * sum before it is added.  Results are bitwise reproducible for fixed arguments.
  *
  * Values.  A NaN or infinite A[i][k] gets the code NaN and makes row i of the result
  * NaN (in sgemm_f32_f8_ta row or column i of its expert's matrix); other rows are not
  * affected.  A NaN code or scale of W makes its columns NaN, an infinite scale
- * NaN or infinite; a scale below 2^-126 can count as zero.  Values of A that
- * round to 2^128 in 8 bits (1.9375 * 2^127, 3.296e38, and more) count as infinite: their
- * rows of the result become infinite or NaN.  Values of A below
+ * NaN or infinite; a block with a scale of zero adds nothing, whatever the rows are.
+ * Values of A that round to 2^128 in 8 bits (1.9375 * 2^127, 3.296e38, and more) count as
+ * infinite: their rows of the result become infinite or NaN.  Values of A below
  * 2^-134 become zero, and below 2^-130 (e4m3) or 2^-131 (e5m2) they have fewer bits
- * than codes have.  Blocks of weights with scales of 2^-100 and less, or of
- * 2^100 and more, can lose bits or overflow where the results do.
+ * than codes have.  A code of W times the power of two in its scale counts as infinite from
+ * 2^128 on and loses its bits below 2^-133.  Beyond that a block's sum is formed with the
+ * powers of two of both scales and then multiplied by what is left of W's, 1 to 2, so
+ * nothing overflows as long as the sums of the terms have room.
  */
 #ifndef SGEMM_F32_F8_H
 #define SGEMM_F32_F8_H
