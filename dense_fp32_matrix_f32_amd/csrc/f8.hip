@@ -201,7 +201,7 @@ __device__ __forceinline__ void f8_tile(const F8Args &p, unsigned char *stage0,
     auto multiply = [&](const unsigned char *s, int b) {
         const unsigned char *xs = s + T::CODES + xrow * 4 + ((block0 + b) & 3);
         const unsigned char *ws = s + T::CODES + (T::BM + wrow) * 4 + ((block0 + b) & 3);
-        // (taken apart here: next to its load it would wait for the copies that were asked for before)
+        // (here a scalar: 233 instead of 234.5 us for 4096 x 4096 x 8192 in bf16)
         const F8Scale scale =
             WS == W_F32 ? f8_split(__builtin_bit_cast(
                               float, __builtin_amdgcn_readfirstlane(__builtin_bit_cast(int, sw))))
@@ -433,7 +433,7 @@ __global__ __launch_bounds__(64 * kFewWaves) void f8_few_kernel(FewArgs f, int r
             codes.half[0] = b.w[c][0];
             codes.half[1] = b.w[c][1];
             bf16x8 w[4];
-            const F8Scale scale = POW2 ? F8Scale{b.s[c], 1.0f} : f8_split(b.s[c]);
+            const F8Scale scale = POW2 ? F8Scale{b.s[c], 1.0f} : f8_split(f8_here(b.s[c]));
             codes.widen<F8_E4M3>(scale.power, w);
 #pragma unroll
             for (int r = 0; r < RT; ++r) {

@@ -47,6 +47,7 @@ struct FourBits {
     __device__ void load(Weights &w, const unsigned char *strip, int, int block) const {
         w.load(strip + (int64_t)block * l.record, at);
     }
+    __device__ void arrived(Weights &) const {}
     __device__ bf16x8 operand(const Weights &w, int j) const { return codes_of(w.word(j)); }
     __device__ float scale(const Weights &w, int t) const { return w.scale_of(t, at); }
     __device__ float zero(const Weights &w, int t) const { return w.zero_of(t, at); }
@@ -82,17 +83,19 @@ struct EightBits {
         w.c[1] = *(const uint4 *)(from + flip);
         w.s = ((const float *)(strip - n * kF8Block + l.planes))[block * l.cols + n / kF8Block];
     }
+    __device__ void arrived(Weights &w) const { w.s = f8_here(w.s); }
     __device__ bf16x8 operand(const Weights &w, int j) const {
         const uint4 c = w.c[j / 2];
         const unsigned lo = j % 2 ? c.z : c.x, hi = j % 2 ? c.w : c.y;
+        const float power = f8_split(w.s).power;
         Frag f;
-        f.pair[0] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, 1.0f, false);
-        f.pair[1] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, 1.0f, true);
-        f.pair[2] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, 1.0f, false);
-        f.pair[3] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, 1.0f, true);
+        f.pair[0] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, power, false);
+        f.pair[1] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, power, true);
+        f.pair[2] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, power, false);
+        f.pair[3] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, power, true);
         return f.v;
     }
-    __device__ float scale(const Weights &w, int) const { return w.s; }
+    __device__ float scale(const Weights &w, int) const { return f8_split(w.s).rest; }
     __device__ float zero(const Weights &, int) const { return 0.0f; }
     static __device__ int put_run(int lane) { return (lane & 31) >> 1; }
     static __device__ int put_half(int lane) { return lane & 1; }
@@ -175,6 +178,8 @@ struct CodesEngine {
             }
             wave_sync();
         }
+#pragma unroll
+        for (int c = 0; c < CT; ++c) f.arrived(b.w[c]);
         const Frag ones{.word = {0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u}};
         constexpr int CS = CT + (F::SUMS ? 1 : 0);
 #pragma unroll

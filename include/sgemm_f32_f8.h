@@ -32,7 +32,7 @@
  * Values.  A NaN or infinite A[i][k] gets the code NaN and makes row i of the result
  * NaN (in sgemm_f32_f8_ta row or column i of its expert's matrix); other rows are not
  * affected.  A NaN code or scale of W makes its columns NaN, an infinite scale
- * NaN or infinite; a block with a scale of zero adds nothing, whatever the rows are.
+ * NaN or infinite; a block with a scale of zero adds nothing, however large the rows.
  * Values of A that round to 2^128 in 8 bits (1.9375 * 2^127, 3.296e38, and more) count as
  * infinite: their rows of the result become infinite or NaN.  Values of A below
  * 2^-134 become zero, and below 2^-130 (e4m3) or 2^-131 (e5m2) they have fewer bits

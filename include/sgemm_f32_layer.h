@@ -23,10 +23,15 @@
  * allocated and no pointer kept; calls can be captured into a HIP graph).
  *
  * Arithmetic is fp32: x and h enter the products without rounding (with weights in 4 or 8
- * bits as in sgemm_f32_w4.h: bits below 2^-133 are dropped, and what it says of large
- * values holds for x and h), sums and activations are fp32.  Results are bitwise
- * reproducible for fixed arguments.  A NaN or infinity in a token's x or weights makes
- * elements of its row of y NaN or infinite; other rows are not affected.
+ * bits but for bits below 2^-133, which are dropped), sums and activations are fp32.
+ * Results are bitwise reproducible for fixed arguments.  A NaN or infinity in a token's x or
+ * weights makes elements of its row of y NaN or infinite; other rows are not affected.
+ *
+ * Large values.  With weights in 4 bits what sgemm_f32_w4.h says of them holds for x and h
+ * (up to 1.7e35 for groups of 128 and more).  With weights in 8 bits the power of two of a scale enters before the sum over its block, so
+ * nothing overflows as long as the sums of the terms have room, and a block with a scale of
+ * zero adds nothing; a code times that power of two counts as infinite from 2^128 on and
+ * loses its bits below 2^-133.
  */
 #ifndef SGEMM_F32_LAYER_H
 #define SGEMM_F32_LAYER_H
