@@ -7,13 +7,14 @@
 // chosen, once each.  Both kernels work on items: up to MR pairs (token, choice) of one expert,
 // MR being the rows that a matrix instruction holds.  In the first a work-group takes one item and a
 // strip of columns of both G and U, whose products meet in its epilogue.  In the second it
-// takes a strip of D's columns and all items in turn, and adds what they give, with its
-// weight, to the tokens' sums in LDS, each wave to its own: nothing is added through
-// memory.  In both the waves take blocks of k in turn and their sums are added at the end,
-// in a fixed order.
+// takes a strip of D's columns and all items in turn, or a share of their blocks of k, and adds
+// what they give, with its weight, to the tokens' sums in LDS, each wave to its own.  Where several
+// work-groups share a strip, as they do where there are few strips for the CUs, each writes
+// its sums to the workspace and a third kernel adds those.  The waves take blocks of k in turn,
+// and whatever is added is added in a fixed order.
 //
 // Up to 64 pairs the kernels find the items themselves; more are sorted by expert first
-// (route.hip), which is a third launch.  More than kLayerTokens tokens go in several rounds.
+// (route.hip), which is a launch more.  More than kLayerTokens tokens go in several rounds.
 #include <initializer_list>
 #include <type_traits>
 
@@ -590,9 +591,13 @@ __global__ __launch_bounds__(W * 64, 2) void layer_up_kernel(LayerProblem p, Hid
 template <class E, int W>
 struct DownLds {
     int tokens, items, list;  // list: places in the pairs' arrays
-    __host__ __device__ int sums() const { return W * E::XS; }
-    __host__ __device__ int items_at() const { return sums() + W * tokens * (E::COLS + 1) * 4; }
-    __host__ __device__ int bytes() const { return items_at() + 3 * items * 4 + 3 * list * 4; }
+    __host__ __device__ constexpr int sums() const { return W * E::XS; }
+    __host__ __device__ constexpr int items_at() const {
+        return sums() + W * tokens * (E::COLS + 1) * 4;
+    }
+    __host__ __device__ constexpr int bytes() const {
+        return items_at() + 3 * items * 4 + 3 * list * 4;
+    }
 };
 
 template <class E, int W, int D>
@@ -871,17 +876,18 @@ int shares(const LayerProblem &p, int cols, int mr, int block, int waves, int64_
     return (int)(n < 1 ? 1 : n < kSplit ? n : kSplit);
 }
 
-// STRIPS strips of y for each work-group, or two where the LDS does not hold the sums of more.
+// STRIPS strips of y for each work-group, or two where the LDS does not hold the sums of more (it
+// holds those of two with the tables of any choices).
 template <class R, class F, int STRIPS>
 hipError_t launch_down_as(const LayerProblem &p, const Hidden &o, int64_t groups, hipStream_t s) {
-    if constexpr (STRIPS > 2) {
-        if (down_lds_of<CodesEngine<R, F, 1, STRIPS>, 8>(p, o).bytes() > kLds)
-            return launch_down_as<R, F, 2>(p, o, groups, s);
-    } else if constexpr (STRIPS == 2) {
-        if (down_lds_of<CodesEngine<R, F, 1, 2>, 8>(p, o).bytes() > kLds)
-            return launch_down_as<R, F, 1>(p, o, groups, s);
-    }
     using E = CodesEngine<R, F, 1, STRIPS>;
+    if constexpr (STRIPS > 2) {
+        if (down_lds_of<E, 8>(p, o).bytes() > kLds)
+            return launch_down_as<R, F, 2>(p, o, groups, s);
+    } else {
+        constexpr int pairs = kLayerTokens * kLayerTop;
+        static_assert(DownLds<E, 8>{kLayerTokens, pairs, pairs}.bytes() <= kLds, "any choices");
+    }
     return launch_down_with<E, 8, 1>(p, o, s, shares(p, E::COLS, E::MR, E::BLOCK, 8, groups));
 }
 

@@ -28,10 +28,10 @@
  * weights makes elements of its row of y NaN or infinite; other rows are not affected.
  *
  * Large values.  With weights in 4 bits what sgemm_f32_w4.h says of them holds for x and h
- * (up to 1.7e35 for groups of 128 and more).  With weights in 8 bits the power of two of a scale enters before the sum over its block, so
- * nothing overflows as long as the sums of the terms have room, and a block with a scale of
- * zero adds nothing; a code times that power of two counts as infinite from 2^128 on and
- * loses its bits below 2^-133.
+ * (up to 1.7e35 for groups of 128 and more).  With weights in 8 bits the power of two of a
+ * scale enters before the sum over its block, so nothing overflows as long as the sums of
+ * the terms have room, and a block with a scale of zero adds nothing; a code times that
+ * power of two counts as infinite from 2^128 on and loses its bits below 2^-133.
  */
 #ifndef SGEMM_F32_LAYER_H
 #define SGEMM_F32_LAYER_H
