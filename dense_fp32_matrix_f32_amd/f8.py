@@ -106,8 +106,9 @@ def _pointer(w):
 
 def f8_pack(codes, scales, stream=None):
     """F8Weights from codes ([experts x] K x N, float8_e4m3fn, row-major or transposed
-    views) and scales ([experts x] ceil(K/128) x ceil(N/128), float32 or float8_e8m0fnu,
-    contiguous, or as transposed views where the codes are)."""
+    views) and scales ([experts x] ceil(K/128) x ceil(N/128), float32 or float8_e8m0fnu, in the
+    codes' layout: contiguous, or with transposed codes the transposed view of a contiguous
+    array, as in ``f8_pack(codes.t(), scales.t())``)."""
     if not isinstance(codes, torch.Tensor) or codes.dim() not in (2, 3):
         raise TypeError("codes must be a 2-D or 3-D float8_e4m3fn torch tensor")
     stacked = codes.dim() == 3
@@ -122,7 +123,9 @@ def f8_pack(codes, scales, stream=None):
         raise ValueError(f"scales has the shape {tuple(scales.shape)}; {shape} is needed")
     held = scales.transpose(-1, -2) if trans else scales
     if not held.is_contiguous():
-        raise ValueError("scales must be contiguous, or a transposed view where codes is one")
+        raise ValueError("scales must be " + ("the transposed view of a contiguous array, as codes is a "
+                                              "transposed one" if trans else
+                                              "contiguous, as codes is row-major"))
     dense(held, held.shape, "scales", scales.dtype, codes.get_device())
     w = _new(experts, stacked, K, N, kind, codes, stream)
     call("sgemm_f32_f8_pack", codes.get_device(), stream, experts, N, K, OP_T if trans else OP_N,
