@@ -9,11 +9,14 @@
 // A wave takes a token.  Lane l holds V logits side by side, l V .. l V + V - 1, as integers in
 // the order of the numbers, sorted largest first with the lowest number first among equal
 // ones.  The largest over the lanes' first ones, in the lowest lane that has it, is the next choice,
-// and that lane moves its list up: about 20 instructions a choice.  Nothing but the
-// logits is read and nothing but the results written; many tokens are bound by the vector
-// work of the sorting and the exponentials (32768 tokens, 8 of 256: choice 23 us, gradient
-// 20, against 7 and 14 to move the bytes; looking at all V logits in every round, and sums
-// over lanes through LDS: 31 and 28; two tokens a wave, eight logits a lane: choice 42).
+// and that lane moves its list up.  Nothing but the logits is read and nothing but the
+// results written; many tokens are bound by vector instructions (32768 tokens, 8 of 256:
+// choice 23 us, gradient 20, against 7 and 14 to move the bytes; looking at all V logits in
+// every round, and sums over lanes through LDS: 31 and 28; two tokens a wave, eight logits a
+// lane: choice 42).  A token of 129 to 256 experts takes 47 of them for each choice, most of
+// them for the steps over the lanes and for the lists, which the compiler moves up by selects over
+// the whole list, 89 for its sort and about 100 for the exponentials and the sums: of 549 two
+// thirds are the choices'.  Up to 512 experts a choice is 151 instructions, up to 1024 it is 647.
 #include "experts.h"
 #include "groups.h"
 

@@ -578,19 +578,21 @@ int64_t rows_each(int rows, int experts, bool by_expert) {
 // types of results are summed alike and differ in their stores only.  Times in us with fp32 / power
 // of two scales:
 //   rows  N x K, result             64 x 64    128 x 128   256 x 256
-//    512  4096 x 4096, fp32          25 / 23     38 / 37    104 / 85
-//   1024  4096 x 4096, fp32          47 / 40     46 / 42    107 / 88
-//   4096  8192 x 4096, fp32         327 / 273   243 / 223   221 / 194
-//   8192  8192 x 8192, fp32        1197 / 1064  920 / 841   857 / 732
-//   2048 by expert, 8 x 4096 x 2048, fp32    49 / 45     51 / 48     62 / 53
-//  16384 by expert, 8 x 2048 x 4096, fp32   338 / 295   273 / 248   327 / 273
-//  16384 by expert, 8 x 4096 x 2048, fp32   363 / 322   280 / 252   302 / 265
-//    512  4096 x 4096, bf16          28 / 23     45 / 37    107 / 89
-//   1024  8192 x 4096, bf16          88 / 73     79 / 64    111 / 92
-//   4096  8192 x 4096, bf16         312 / 272   259 / 218   217 / 193
-//   8192  8192 x 8192, bf16        1200 / 1051  977 / 832   823 / 724
-//   2048 by expert, 32 x 2048 x 1024, bf16   22 / 19     24 / 21     34 / 29
-//  16384 by expert, 8 x 4096 x 2048, bf16   346 / 311   292 / 252   295 / 258
+//    512  4096 x 4096, fp32          25 / 21     40 / 35    104 / 85
+//   1024  4096 x 4096, fp32          47 / 40     47 / 43    107 / 89
+//   4096  8192 x 4096, fp32         335 / 270   247 / 230   221 / 194
+//   8192  8192 x 8192, fp32        1241 / 1075  944 / 851   852 / 734
+//   2048 by expert, 8 x 4096 x 2048, fp32    50 / 44     52 / 47     61 / 52
+//  16384 by expert, 8 x 2048 x 4096, fp32   345 / 296   272 / 247   320 / 270
+//  16384 by expert, 8 x 4096 x 2048, fp32   372 / 319   288 / 252   298 / 257
+//    512  4096 x 4096, bf16          29 / 23     47 / 38    107 / 90
+//   1024  8192 x 4096, bf16          92 / 73     79 / 64    109 / 92
+//   4096  8192 x 4096, bf16         322 / 270   261 / 221   219 / 190
+//   8192  8192 x 8192, bf16        1220 / 1057  984 / 832   827 / 722
+//   2048 by expert, 32 x 2048 x 1024, bf16   23 / 19     25 / 20     34 / 28
+//  16384 by expert, 8 x 4096 x 2048, bf16   354 / 316   293 / 252   294 / 254
+// (4096 rows of 8192 x 4096 are 228 us at the rate that a bf16 product of the library reaches, 1203
+// TFLOP/s.)
 template <int XT, class OUT>
 hipError_t launch_many(const F8Problem &p, const F8Args &a, hipStream_t s) {
     const bool by_expert = p.offsets != nullptr;
